@@ -22,6 +22,7 @@ F32, BF16, E4M3, E2M1, E4M3R = 0, 1, 2, 3, 4
 DTYPES = {"f32": F32, "bf16": BF16, "e4m3": E4M3, "e2m1": E2M1, "e4m3r": E4M3R}
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_BOUNDS, ERR_WORKSPACE, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5, -6
+ERR_NONFINITE = -7
 
 
 class CsaError(RuntimeError):
@@ -51,11 +52,23 @@ class Layer(ctypes.Structure):
                 ("rope_theta", ctypes.c_float), ("rms_eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
+class Kv8C(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("rows_per_block", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class Kv8MaskC(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("first", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
 _lib = None
 
-_VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_VP, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _PP, _PB, _PL = ctypes.POINTER(Paged), ctypes.POINTER(BlockTableC), ctypes.POINTER(Layer)
 _PQ = ctypes.POINTER(QueryNormC)
+_PK, _PM = ctypes.POINTER(Kv8C), ctypes.POINTER(Kv8MaskC)
 
 _SIGS = {
     "csa_compress_insert": (_I32, [_PL, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _PP, _PB, _PP, _PB, _PP,
@@ -73,6 +86,12 @@ _SIGS = {
     "csa_sparse_attn_workspace_size": (_SZ, [_PL, _I32, _I32]),
     "csa_indexer_topk_noalloc": (_I32, [_VP, _I32, _VP, _I32, _I32, _I32, _VP, _VP, _I32, _I32, _PP, _PB, _I32,
                                         _I32, _VP, _VP, _VP]),
+    "csa_step_plan": (_I32, [_VP, _VP, _I32, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP,
+                             _VP]),
+    "csa_kv8_store": (_I32, [_VP, _VP, _I32, _I64, _I64, _I32, _VP, _VP, _PK, _PB, _VP, _VP]),
+    "csa_kv8_attn": (_I32, [_VP, _I32, _I64, _I32, _I32, _VP, _VP, _I32, _PK, _PB, _PM, _VP, _I32, _VP, _VP, _SZ,
+                            _VP, _VP]),
+    "csa_kv8_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _PK, _I32]),
     "csa_read_status": (_I32, [_VP, _I32, _VP]),
     "csa_status_string": (ctypes.c_char_p, [_I32]),
     "csa_version": (_I32, []),
@@ -295,6 +314,151 @@ def sparse_attn_prefill(layer: Layer, q, seq_id, pos, comp: PagedCache, comp_bt,
                         swa: PagedCache, swa_bt, out, out_dtype: int, out_scales, ws, err, stream=None):
     _attn("csa_sparse_attn_prefill", layer, q, seq_id, pos, comp, comp_bt, topk, k, max_n, swa, swa_bt, out,
           out_dtype, out_scales, ws, err, stream)
+
+
+# ------------------------------------------------------------------ step plan, 8-bit key / value cache
+
+
+def _dev(t, dtype, what, device):
+    """Device pointer of a dense tensor of the given type on `device`."""
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must live on the current CUDA device")
+    return t.data_ptr()
+
+
+def _rows3(t, what, device):
+    """(pointer, elements between rows) of [rows, heads, dim] rows whose heads are dense."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] != 1):
+        raise ValueError(f"{what} must be [rows, heads, dim] with dense heads")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must live on the current CUDA device")
+    return t.data_ptr(), t.stride(0)
+
+
+@dataclass
+class Kv8Cache:
+    """A paged key / value cache in 8 bits: e4m3 codes (uint8) [num_blocks, kv_heads, rows_per_block, dim]
+    and one float scale for each block and head [num_blocks, kv_heads], for keys and for values."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        shape = tuple(self.k.shape)
+        if len(shape) != 4 or tuple(self.v.shape) != shape:
+            raise ValueError("k and v must be [num_blocks, kv_heads, rows_per_block, dim]")
+        if tuple(self.k_scale.shape) != shape[:2] or tuple(self.v_scale.shape) != shape[:2]:
+            raise ValueError("scales must be [num_blocks, kv_heads]")
+        for t, dt in ((self.k, torch.uint8), (self.v, torch.uint8), (self.k_scale, torch.float32),
+                      (self.v_scale, torch.float32)):
+            if t.dtype is not dt:
+                raise ValueError("codes are uint8 and scales float32")
+            if t.device != self.k.device:
+                raise ValueError("the cache's tensors must live on one device")
+        self.num_blocks, self.kv_heads, self.rows_per_block, self.dim = shape
+        self._c = Kv8C(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), shape[0], shape[2],
+                       shape[1], shape[3])
+
+    @staticmethod
+    def empty(num_blocks: int, kv_heads: int, rows_per_block: int, dim: int, device="cuda") -> "Kv8Cache":
+        codes = [torch.zeros(num_blocks, kv_heads, rows_per_block, dim, dtype=torch.uint8, device=device)
+                 for _ in range(2)]
+        scales = [torch.zeros(num_blocks, kv_heads, dtype=torch.float32, device=device) for _ in range(2)]
+        return Kv8Cache(*codes, *scales)
+
+    def c(self) -> Kv8C:
+        return self._c
+
+
+def step_plan(cached, n_new, free_blocks, bt, block_positions: int, num_blocks: int, row_start, seq_id, pos, slot,
+              used, err, stream=None):
+    """Row starts, sequence ids, positions, slots and the block table of a step from its requests' lengths
+    (slot may be None).  bt [num_reqs, stride] is updated in place; rows past the step's become padding (-1)."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    if bt.dim() != 2 or cached.numel() != bt.shape[0] or n_new.numel() != bt.shape[0]:
+        raise ValueError("cached and n_new must have one entry for each row of the block table")
+    if row_start.numel() != bt.shape[0] + 1 or pos.numel() != seq_id.numel() or used.numel() != 1:
+        raise ValueError("row_start must be [num_reqs + 1], seq_id and pos of one length, used [1]")
+    if slot is not None and slot.numel() != seq_id.numel():
+        raise ValueError("slot must have the length of seq_id")
+    st = lib().csa_step_plan(_dev(cached, i32, "cached", dev), _dev(n_new, i32, "n_new", dev), bt.shape[0],
+                             _dev(free_blocks, i32, "free_blocks", dev), free_blocks.numel(),
+                             _dev(bt, i32, "block table", dev), bt.shape[1], block_positions, num_blocks,
+                             seq_id.numel(), _dev(row_start, i32, "row_start", dev), _dev(seq_id, i32, "seq_id", dev),
+                             _dev(pos, i32, "pos", dev),
+                             None if slot is None else _dev(slot, torch.int64, "slot", dev),
+                             _dev(used, i32, "used", dev), _dev(err, i32, "err", dev), _stream(stream))
+    _check(st, "csa_step_plan")
+
+
+def _kv8_lengths(row_start, cached, cache, bt, dev):
+    """Pointers of row_start and cached, and the C block table, checked against each other."""
+    if cache.k.get_device() != dev:
+        raise ValueError("the cache must live on the current CUDA device")
+    if bt.dim() != 2 or row_start.numel() != bt.shape[0] + 1 or cached.numel() != bt.shape[0]:
+        raise ValueError("row_start must be [num_seqs + 1] and cached [num_seqs] for the block table's num_seqs")
+    i32 = torch.int32
+    return (_dev(row_start, i32, "row_start", dev), _dev(cached, i32, "cached", dev),
+            BlockTableC(_dev(bt, i32, "block table", dev), bt.shape[0], bt.shape[1]))
+
+
+def kv8_store(k, v, row_start, cached, cache: Kv8Cache, bt, err, stream=None):
+    """Insert k, v [n_rows, kv_heads, dim] (f32 or bf16; rows may be strided) into the 8-bit cache: request b's
+    rows row_start[b]..row_start[b+1] go to positions cached[b].. of row b of the block table."""
+    dev = torch.cuda.current_device()
+    if k.shape != v.shape or k.dtype is not v.dtype:
+        raise ValueError("k and v must have one shape and type")
+    kp, ks = _rows3(k, "k", dev)
+    vp, vs = _rows3(v, "v", dev)
+    if k.shape[1] != cache.kv_heads or k.shape[2] != cache.dim:
+        raise ValueError("k and v must have the cache's heads and dim")
+    rs, ca, b = _kv8_lengths(row_start, cached, cache, bt, dev)
+    st = lib().csa_kv8_store(kp, vp, _tdtype(k), ks, vs, k.shape[0], rs, ca, cache.c(), b,
+                             _dev(err, torch.int32, "err", dev), _stream(stream))
+    _check(st, "csa_kv8_store")
+
+
+def kv8_attn_workspace_size(n_rows: int, num_seqs: int, heads: int, cache: Kv8Cache, max_new: int) -> int:
+    return int(lib().csa_kv8_attn_workspace_size(n_rows, num_seqs, heads, cache.c(), max_new))
+
+
+def kv8_attn(q, row_start, cached, cache: Kv8Cache, bt, max_new: int, out, ws, err, scale: float | None = None,
+             softcap: float = 0.0, window: int = 0, slopes=None, first=None, prefix=None, lse=None, stream=None):
+    """Attention of q [n_rows, heads, dim] (f32 or bf16; rows may be strided) over the 8-bit cache into out
+    [n_rows, heads, dim] (f32 or bf16) and, if given, lse [n_rows, heads] (float).  Scores are capped by
+    softcap * tanh(a / softcap), lowered by slopes[head] * distance, and masked by causality, `window`, `first`
+    (int32 [n_rows], each row's first visible position) and `prefix` (int32 [num_seqs], tokens every row sees).
+    The cache already holds the rows' own tokens; max_new is the most rows of a request."""
+    dev = torch.cuda.current_device()
+    qp, qs = _rows3(q, "q", dev)
+    n_rows, heads, dim = q.shape
+    if dim != cache.dim or out.shape != q.shape:
+        raise ValueError("q and out must be [n_rows, heads, dim] with the cache's dim")
+    rs, ca, b = _kv8_lengths(row_start, cached, cache, bt, dev)
+    i32, f32 = torch.int32, torch.float32
+    if slopes is not None and slopes.numel() != heads:
+        raise ValueError("slopes must be [heads]")
+    if first is not None and first.numel() != n_rows:
+        raise ValueError("first must be [n_rows]")
+    if prefix is not None and prefix.numel() != bt.shape[0]:
+        raise ValueError("prefix must be [num_seqs]")
+    if lse is not None and lse.numel() != n_rows * heads:
+        raise ValueError("lse must be [n_rows, heads]")
+    m = Kv8MaskC(dim ** -0.5 if scale is None else scale, softcap, window,
+                 None if slopes is None else _dev(slopes, f32, "slopes", dev),
+                 None if first is None else _dev(first, i32, "first", dev),
+                 None if prefix is None else _dev(prefix, i32, "prefix", dev))
+    st = lib().csa_kv8_attn(qp, _tdtype(q), qs, n_rows, heads, rs, ca, max_new, cache.c(), b, m,
+                            _dev(out, out.dtype, "out", dev), _tdtype(out),
+                            None if lse is None else _dev(lse, f32, "lse", dev),
+                            None if ws is None else _dev(ws, ws.dtype, "ws", dev),
+                            0 if ws is None else ws.numel() * ws.element_size(), _dev(err, i32, "err", dev),
+                            _stream(stream))
+    _check(st, "csa_kv8_attn")
 
 
 def read_status(err, reset: bool = True, stream=None) -> int:

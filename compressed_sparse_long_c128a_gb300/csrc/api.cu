@@ -33,6 +33,16 @@ int check_paged(const csa_paged* c, int32_t dim, int32_t rows_per_block, unsigne
   return CSA_OK;
 }
 
+int check_kv8(const csa_kv8* c) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->num_blocks <= 0) return CSA_ERR_INVALID_ARG;
+  if (c->kv_heads <= 0 || c->dim <= 0 || c->rows_per_block <= 0) return CSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) % 16) return CSA_ERR_INVALID_ARG;
+  const int32_t r = c->rows_per_block;
+  if (r < 16 || r > 256 || (r & (r - 1)) || c->dim % 16 || c->dim > 256 || c->kv_heads > 65535)
+    return CSA_ERR_UNSUPPORTED;
+  return CSA_OK;
+}
+
 int check_bt(const csa_block_table* bt) {
   if (!bt || !bt->table || bt->num_seqs <= 0 || bt->stride <= 0) return CSA_ERR_INVALID_ARG;
   return CSA_OK;
@@ -383,6 +393,91 @@ int csa_sparse_attn_prefill(const csa_layer* L, const void* q, int32_t q_dtype, 
                      out_dtype, out_scales, ws, ws_bytes, err, stream);
 }
 
+int csa_step_plan(const int32_t* cached, const int32_t* n_new, int32_t num_reqs, const int32_t* free_blocks,
+                  int32_t n_free, int32_t* table, int32_t stride, int32_t block_positions, int32_t num_blocks,
+                  int32_t n_rows, int32_t* row_start, int32_t* seq_id, int32_t* pos, int64_t* slot, int32_t* used,
+                  int32_t* err, csa_stream_t stream) {
+  if (num_reqs < 0 || n_free < 0 || n_rows < 0 || stride <= 0 || block_positions <= 0 || num_blocks <= 0)
+    return CSA_ERR_INVALID_ARG;
+  if (!row_start || !used || !err || (num_reqs > 0 && (!cached || !n_new || !table)) || (n_free > 0 && !free_blocks) ||
+      (n_rows > 0 && (!seq_id || !pos)))
+    return CSA_ERR_INVALID_ARG;
+  PlanArgs a{cached, n_new, num_reqs, free_blocks, n_free, table, stride, block_positions, num_blocks, n_rows,
+             row_start, seq_id, pos, slot, used, err};
+  return cuda_status(launch_plan(a, stream));
+}
+
+int csa_kv8_store(const void* k, const void* v, int32_t in_dtype, int64_t k_stride, int64_t v_stride, int32_t n_rows,
+                  const int32_t* row_start, const int32_t* cached, const csa_kv8* cache, const csa_block_table* bt,
+                  int32_t* err, csa_stream_t stream) {
+  if (n_rows < 0 || k_stride < 0 || v_stride < 0) return CSA_ERR_INVALID_ARG;
+  if (n_rows == 0) return CSA_OK;
+  if (!k || !v || !row_start || !cached || !err) return CSA_ERR_INVALID_ARG;
+  if (in_dtype != CSA_F32 && in_dtype != CSA_BF16) return CSA_ERR_UNSUPPORTED;
+  int st = check_kv8(cache);
+  if (st) return st;
+  if ((st = check_bt(bt))) return st;
+  if ((int64_t)n_rows / cache->rows_per_block + bt->num_seqs > INT32_MAX) return CSA_ERR_UNSUPPORTED;
+  const size_t el = in_dtype == CSA_F32 ? 4 : 2;
+  const uintptr_t al = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
+  if (al % el) return CSA_ERR_INVALID_ARG;
+  Kv8StoreArgs a{{k, v}, {k_stride, v_stride}, in_dtype, n_rows, row_start, cached, *cache, *bt, 0, err};
+  a.vec = al % 16 == 0 && k_stride * el % 16 == 0 && v_stride * el % 16 == 0;
+  return cuda_status(launch_kv8_store(a, stream));
+}
+
+size_t csa_kv8_attn_workspace_size(int32_t n_rows, int32_t num_seqs, int32_t heads, const csa_kv8* cache,
+                                   int32_t max_new) {
+  if (!cache || n_rows <= 0 || num_seqs <= 0 || heads <= 0 || cache->kv_heads <= 0 || cache->dim <= 0 || max_new <= 0)
+    return 0;
+  return align_up(
+      kv8_simt_workspace(n_rows, heads, cache->dim, kv8_simt_splits(n_rows, heads, cache->kv_heads)));
+}
+
+int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_rows, int32_t heads,
+                 const int32_t* row_start, const int32_t* cached, int32_t max_new, const csa_kv8* cache,
+                 const csa_block_table* bt, const csa_kv8_mask* mask, void* out, int32_t out_dtype, float* lse,
+                 void* ws, size_t ws_bytes, int32_t* err, csa_stream_t stream) {
+  if (n_rows < 0 || max_new < 0 || heads <= 0 || q_stride < 0) return CSA_ERR_INVALID_ARG;
+  if (n_rows == 0 || max_new == 0) return CSA_OK;
+  if (!q || !row_start || !cached || !mask || !out || !err) return CSA_ERR_INVALID_ARG;
+  if ((q_dtype != CSA_F32 && q_dtype != CSA_BF16) || (out_dtype != CSA_F32 && out_dtype != CSA_BF16))
+    return CSA_ERR_UNSUPPORTED;
+  int st = check_kv8(cache);
+  if (st) return st;
+  if ((st = check_bt(bt))) return st;
+  if (heads % cache->kv_heads) return CSA_ERR_INVALID_ARG;
+  if (!(mask->scale > 0.f) || !std::isfinite(mask->scale) || !(mask->softcap >= 0.f) || !std::isfinite(mask->softcap) ||
+      mask->window < 0)
+    return CSA_ERR_INVALID_ARG;
+  if (heads > 65535) return CSA_ERR_UNSUPPORTED;
+  const size_t q_el = q_dtype == CSA_F32 ? 4 : 2, o_el = out_dtype == CSA_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(q) % q_el || reinterpret_cast<uintptr_t>(out) % o_el) return CSA_ERR_INVALID_ARG;
+  const size_t need = csa_kv8_attn_workspace_size(n_rows, bt->num_seqs, heads, cache, max_new);
+  if (need && (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16)) return CSA_ERR_WORKSPACE;
+  Kv8AttnArgs a{};
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.q_stride = q_stride;
+  a.n_rows = n_rows;
+  a.heads = heads;
+  a.group = heads / cache->kv_heads;
+  a.row_start = row_start;
+  a.cached = cached;
+  a.max_new = max_new;
+  a.cache = *cache;
+  a.bt = *bt;
+  a.mask = *mask;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.lse = lse;
+  a.n_splits = kv8_simt_splits(n_rows, heads, cache->kv_heads);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = a.part_o + (size_t)n_rows * heads * a.n_splits * cache->dim;
+  a.err = err;
+  return cuda_status(launch_kv8_attn_simt(a, stream));
+}
+
 int csa_read_status(int32_t* err, int32_t reset, csa_stream_t stream) {
   if (!err) return CSA_ERR_INVALID_ARG;
   int32_t v = 0;
@@ -404,6 +499,7 @@ const char* csa_status_string(int32_t s) {
     case CSA_ERR_DEVICE_BOUNDS: return "device: unmapped or out-of-range block or index";
     case CSA_ERR_WORKSPACE: return "workspace too small";
     case CSA_ERR_TIMEOUT: return "device: a bounded wait gave up";
+    case CSA_ERR_NONFINITE: return "device: a NaN or an infinity in rows to be quantised";
     default: return "unknown status";
   }
 }

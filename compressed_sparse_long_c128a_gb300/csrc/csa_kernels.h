@@ -266,4 +266,60 @@ bool attn_tc_eligible(const AttnArgs& a);
 int32_t attn_tc_splits(int32_t n_rows, int32_t keys_per_row);
 cudaError_t launch_attn_tc(const AttnArgs& a, int32_t n_rows, cudaStream_t s);
 
+// ---- step plan (k_plan.cu)
+struct PlanArgs {
+  const int32_t* cached;
+  const int32_t* n_new;
+  int32_t num_reqs;
+  const int32_t* free_blocks;
+  int32_t n_free;
+  int32_t* table;
+  int32_t stride, block_positions, num_blocks, n_rows;
+  int32_t* row_start;
+  int32_t* seq_id;
+  int32_t* pos;
+  int64_t* slot;  // nullptr: not wanted
+  int32_t* used;
+  int32_t* err;
+};
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s);
+
+// ---- 8-bit key / value cache of grouped-query layers (k_kv8_store.cu, k_kv8_attn.cu)
+struct Kv8StoreArgs {
+  const void* x[2];  // keys, values
+  int64_t stride[2];
+  int32_t in_dtype, n_rows;
+  const int32_t* row_start;
+  const int32_t* cached;
+  csa_kv8 cache;
+  csa_block_table bt;
+  int32_t vec;  // rows may be read 16 bytes at a time
+  int32_t* err;
+};
+cudaError_t launch_kv8_store(const Kv8StoreArgs& a, cudaStream_t s);
+
+struct Kv8AttnArgs {
+  const void* q;
+  int32_t q_dtype;
+  int64_t q_stride;
+  int32_t n_rows, heads, group;  // group: query heads a key head
+  const int32_t* row_start;
+  const int32_t* cached;
+  int32_t max_new;
+  csa_kv8 cache;
+  csa_block_table bt;
+  csa_kv8_mask mask;
+  void* out;
+  int32_t out_dtype;
+  float* lse;
+  float* part_o;  // partial results, see the kernels
+  float* part_ml;
+  int32_t n_splits;
+  int32_t* err;
+};
+// CUDA-core kernel, any type and dim: splits of a row's keys, and its scratch
+int32_t kv8_simt_splits(int32_t n_rows, int32_t heads, int32_t kv_heads);
+size_t kv8_simt_workspace(int32_t n_rows, int32_t heads, int32_t dim, int32_t n_splits);
+cudaError_t launch_kv8_attn_simt(const Kv8AttnArgs& a, cudaStream_t s);
+
 }  // namespace csa

@@ -1,0 +1,195 @@
+// Block tables and slot maps of a serving step, from its requests' lengths.
+//
+// With n_b new tokens and d_b = ceil((cached_b + n_b) / P) - ceil(cached_b / P) new
+// blocks, everything follows from two exclusive prefix sums over the requests, of
+// n (a row's request and place) and of d (a new block's place among the free ones).
+// The call moves a few hundred KB at most, so latency bounds it: one launch, in which
+// every CTA forms the sums again from the 8 bytes a request (L2 hits) rather than
+// wait for another CTA's.  Thread t sums a contiguous segment of ceil(B / 512)
+// requests, one block-wide scan turns these into the segments' prefixes (kept in
+// shared memory, whatever B is), and a row or a table line finds its request by a
+// binary search over the segments and a walk inside one.
+
+#include "csa_kernels.h"
+
+namespace csa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRowsPerThread = 4;
+
+struct Req {
+  int64_t n;        // new tokens, 0 for a request that does not fit
+  int32_t cached;   // 0 if negative
+  int32_t held, take;  // blocks held, and taken (within the table)
+  bool bad;
+};
+
+__device__ __forceinline__ Req load_req(const PlanArgs& a, int b) {
+  Req r;
+  const int32_t c = a.cached[b], n = a.n_new[b];
+  r.bad = c < 0 || n < 0 || (int64_t)c + n > INT32_MAX;
+  r.cached = max(c, 0);
+  r.n = r.bad ? 0 : n;
+  const int64_t P = a.block_positions;
+  const int64_t held = ((int64_t)r.cached + P - 1) / P, need = ((int64_t)r.cached + r.n + P - 1) / P;
+  r.bad |= need > a.stride;
+  r.held = (int32_t)min(held, (int64_t)a.stride);
+  r.take = (int32_t)(min(need, (int64_t)a.stride) - r.held);
+  return r;
+}
+
+// Physical block of logical block lb of a request whose new blocks start at free
+// block `took`; -1 where there is none.
+__device__ __forceinline__ int32_t block_at(const PlanArgs& a, int b, const Req& r, int64_t took, int64_t lb) {
+  if (lb >= a.stride) return -1;
+  int32_t id = -1;
+  if (lb < r.held) {
+    id = a.table[(int64_t)b * a.stride + lb];
+  } else {
+    const int64_t f = took + lb - r.held;
+    if (f < a.n_free) id = a.free_blocks[f];
+  }
+  return id >= 0 && id < a.num_blocks ? id : -1;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
+  __shared__ int64_t seg_n[kThreads + 1], seg_d[kThreads + 1];  // exclusive prefixes of the segments
+  __shared__ int64_t warp_n[kThreads / 32], warp_d[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int B = a.num_reqs;
+  const int seg = (B + kThreads - 1) / kThreads;  // requests a thread
+  const int b0 = min(B, tid * seg), b1 = min(B, b0 + seg);
+  int64_t sn = 0, sd = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const Req r = load_req(a, b);
+    sn += r.n;
+    sd += r.take;
+    bad |= r.bad;
+  }
+  int64_t n = sn, d = sd;  // inclusive scan
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t un = __shfl_up_sync(0xffffffffu, n, o), ud = __shfl_up_sync(0xffffffffu, d, o);
+    if (lane >= o) n += un, d += ud;
+  }
+  if (lane == 31) warp_n[wid] = n, warp_d[wid] = d;
+  __syncthreads();
+  int64_t bn = 0, bd = 0;
+  for (int w = 0; w < wid; ++w) bn += warp_n[w], bd += warp_d[w];
+  seg_n[tid] = bn + n - sn;
+  seg_d[tid] = bd + d - sd;
+  if (tid == kThreads - 1) seg_n[kThreads] = bn + n, seg_d[kThreads] = bd + d;
+  __syncthreads();
+  const int64_t total = seg_n[kThreads], taken = seg_d[kThreads];
+
+  if (blockIdx.x == 0) {
+    int64_t s = seg_n[tid];
+    for (int b = b0; b < b1; ++b) {
+      a.row_start[b] = (int32_t)min(s, (int64_t)a.n_rows);
+      s += load_req(a, b).n;
+    }
+    if (tid == 0) {
+      a.row_start[B] = (int32_t)min(total, (int64_t)a.n_rows);
+      a.used[0] = (int32_t)min(taken, (int64_t)a.n_free);
+    }
+    if (bad || (tid == 0 && (total > a.n_rows || taken > a.n_free))) record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
+  }
+
+  // table lines, a warp each: entries past those held
+  const int n_warps = gridDim.x * (kThreads / 32);
+  for (int b = blockIdx.x * (kThreads / 32) + wid; b < B; b += n_warps) {
+    const int s = b / seg;
+    int64_t took = seg_d[s];
+    for (int x = s * seg; x < b; ++x) took += load_req(a, x).take;
+    const Req r = load_req(a, b);
+    for (int j = r.held + lane; j < a.stride; j += 32) {
+      int32_t id = -1;
+      if (j < r.held + r.take) {
+        id = block_at(a, b, r, took, j);
+        if (id < 0) record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
+      }
+      a.table[(int64_t)b * a.stride + j] = id;
+    }
+  }
+
+  // rows, four consecutive ones a thread
+  for (int64_t base = ((int64_t)blockIdx.x * kThreads + tid) * kRowsPerThread; base < a.n_rows;
+       base += (int64_t)gridDim.x * kThreads * kRowsPerThread) {
+    int b = B;
+    int64_t took = 0, end = 0;  // of request b: its first free block, the row behind its last
+    Req r{};
+    if (base < total) {
+      int lo = 0, hi = kThreads;  // the last segment that starts at or before the row
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seg_n[mid] <= base) lo = mid; else hi = mid;
+      }
+      b = lo * seg;
+      took = seg_d[lo];
+      end = seg_n[lo];
+      for (;; ++b) {
+        r = load_req(a, b);
+        end += r.n;
+        if (end > base) break;
+        took += r.take;
+      }
+    }
+    int32_t o_seq[kRowsPerThread], o_pos[kRowsPerThread];
+    int64_t o_slot[kRowsPerThread];
+    int64_t lb = -1;
+    int32_t id = -1;
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int64_t row = base + i;
+      o_seq[i] = o_pos[i] = -1;
+      o_slot[i] = -1;
+      if (row >= total || row >= a.n_rows) continue;
+      while (row >= end) {
+        took += r.take;
+        r = load_req(a, ++b);
+        end += r.n;
+        lb = -1;
+      }
+      const int32_t p = (int32_t)(r.cached + (row - (end - r.n)));
+      o_seq[i] = b;
+      o_pos[i] = p;
+      if (a.slot) {
+        const int32_t l = p / a.block_positions;
+        if (l != lb) {
+          lb = l;
+          id = block_at(a, b, r, took, l);
+          if (id < 0) record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
+        }
+        if (id >= 0) o_slot[i] = (int64_t)id * a.block_positions + (p - l * a.block_positions);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      if (base + i >= a.n_rows) break;
+      a.seq_id[base + i] = o_seq[i];
+      a.pos[base + i] = o_pos[i];
+      if (a.slot) a.slot[base + i] = o_slot[i];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  // a CTA takes 16 table lines or 2048 rows before it loops, up to one CTA an SM
+  const int64_t lines = ((int64_t)a.num_reqs + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t rows = ((int64_t)a.n_rows + kThreads * kRowsPerThread - 1) / (kThreads * kRowsPerThread);
+  int64_t grid = lines > rows ? lines : rows;
+  if (grid > sms) grid = sms;
+  if (grid < 1) grid = 1;
+  return launch_k(plan_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, 0, a);
+}
+
+}  // namespace csa

@@ -61,7 +61,8 @@ typedef enum {
   CSA_ERR_CUDA = -3,          /* a CUDA runtime call or launch failed */
   CSA_ERR_DEVICE_BOUNDS = -4, /* device: unmapped / out-of-range block or index */
   CSA_ERR_WORKSPACE = -5,     /* workspace smaller than the matching *_workspace_size */
-  CSA_ERR_TIMEOUT = -6        /* device: a bounded wait inside a kernel gave up */
+  CSA_ERR_TIMEOUT = -6,       /* device: a bounded wait inside a kernel gave up */
+  CSA_ERR_NONFINITE = -7      /* device: a NaN or an infinity in rows to be quantised */
 } csa_status;
 
 typedef enum {
@@ -315,6 +316,127 @@ CSA_API int csa_indexer_topk_noalloc(const void* q_idx, int32_t q_dtype, const f
                                      const int32_t* pos, int32_t ratio, int32_t window,
                                      const csa_paged* idx_cache, const csa_block_table* bt, int32_t k,
                                      int32_t max_n, int32_t* out_idx, int32_t* err, csa_stream_t stream);
+
+/*
+ * csa_step_plan -- what a serving step's calls take, built on the device from
+ * the lengths of its requests: request b has cached[b] tokens in its cache and
+ * n_new[b] new ones in this step (0 is allowed).  With P = block_positions,
+ * held = ceil(cached / P) and need = ceil((cached + n_new) / P):
+ *   row_start[b]  = n_new[0] + .. + n_new[b-1], for b = 0 .. num_reqs
+ *   seq_id[r], pos[r] = b, cached[b] + (r - row_start[b]) for the rows r of request b
+ *   table[b][j]   = kept for j < held, the next unused free block for held <= j < need
+ *                   (requests take free_blocks[0..n_free) in order), -1 for need <= j < stride
+ *   slot[r]       = table[b][pos / P] * P + pos % P, the row's place in a cache of P-row blocks
+ *   used[0]       = the free blocks taken
+ * Rows r of [row_start[num_reqs], n_rows) are padding: seq_id, pos and slot -1.
+ * One table serves every cache whose logical block covers P positions (256 for
+ * the compressed, window, state and indexer caches; rows_per_block of a csa_kv8).
+ * The table is the only buffer that is read and written, and the entries that
+ * are read (j < held) are not written, so a call can be repeated.
+ *   cached, n_new [num_reqs]; free_blocks [n_free] (NULL when n_free is 0)
+ *   table [num_reqs][stride] int32; row_start [num_reqs + 1]; used [1]
+ *   seq_id, pos [n_rows] int32; slot [n_rows] int64, or NULL
+ * Device conditions (CSA_ERR_DEVICE_BOUNDS): a negative length, or a request past
+ * 2^31 - 1 positions, counts as no new tokens; rows past n_rows are dropped
+ * (row_start is clipped to n_rows); a block past the table's stride, past the free
+ * blocks or outside [0, num_blocks) is left unmapped (-1), and so are its slots.
+ */
+CSA_API int csa_step_plan(const int32_t* cached, const int32_t* n_new, int32_t num_reqs,
+                          const int32_t* free_blocks, int32_t n_free, int32_t* table, int32_t stride,
+                          int32_t block_positions, int32_t num_blocks, int32_t n_rows, int32_t* row_start,
+                          int32_t* seq_id, int32_t* pos, int64_t* slot, int32_t* used, int32_t* err,
+                          csa_stream_t stream);
+
+/*
+ * A paged key / value cache of a grouped-query layer in 8 bits: e4m3 codes
+ * [num_blocks][kv_heads][rows_per_block][dim] for keys and for values, and one
+ * fp32 scale for each block and head, [num_blocks][kv_heads]: value = code * scale.
+ * rows_per_block is 16, 32, 64, 128 or 256; dim a multiple of 16, 16 .. 256; k and v
+ * are 16-byte aligned.  Scales start at zero; csa_kv8_store never writes the NaN
+ * codes 0x7f and 0xff, and rows that hold tokens must not hold them.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_blocks;
+  int32_t rows_per_block;
+  int32_t kv_heads;
+  int32_t dim;
+} csa_kv8;
+
+/*
+ * csa_kv8_store -- insert a step's keys and values, quantising them to e4m3 with
+ * the scale of their block and head.  Request b is row b of the block table: its
+ * rows [row_start[b], row_start[b+1]) go to positions cached[b], cached[b]+1, ..
+ * For each block and head that gets rows, separately for keys and values,
+ *   was   = 0 if the block's first row is among them (a block taken anew), else its scale
+ *   scale = max(was, amax / 448, 2^-100)         amax over the new rows
+ *   code  = e4m3_rn_satfinite(x * (1 / scale))   for the new rows
+ * and, where scale > was, the block's rows before the first new one become
+ *   code  = e4m3_rn_satfinite(code * (was * (1 / scale))).
+ * Rows after the last new one, and other blocks, stay as they were.  All in fp32.
+ * A NaN is stored as 0 and an infinity as the block's largest value, neither
+ * counts in amax, and both set CSA_ERR_NONFINITE.  Two requests of a call must not
+ * write the same physical block.
+ *   k, v  [n_rows][kv_heads][dim] in_dtype (F32 or BF16), rows k_stride / v_stride
+ *         elements apart (key and value may be parts of one projection's rows)
+ *   row_start [num_seqs + 1], cached [num_seqs] int32, as csa_step_plan writes them
+ * A request whose rows are out of order or past n_rows, or whose tokens pass the
+ * table, is skipped, as is an unmapped block (CSA_ERR_DEVICE_BOUNDS).
+ */
+CSA_API int csa_kv8_store(const void* k, const void* v, int32_t in_dtype, int64_t k_stride, int64_t v_stride,
+                          int32_t n_rows, const int32_t* row_start, const int32_t* cached,
+                          const csa_kv8* cache, const csa_block_table* bt, int32_t* err,
+                          csa_stream_t stream);
+
+/*
+ * How the scores of csa_kv8_attn are formed and which keys a row sees.  For the
+ * row at position p of a request and the key at position t,
+ *   a = scale * (q . k);  if softcap > 0: a = softcap * tanh(a / softcap);
+ *   if slopes: a -= slopes[head] * |p - t|
+ * and the row sees the key iff t < cached + n_new, t >= first[row] and either
+ * t < prefix[request], or t <= p and (window == 0 or p - t < window).
+ *   first  the row's document starts there: packed documents see no other one
+ *   prefix tokens that every row sees, before it or behind it (a prompt read in both
+ *          directions; the first tokens kept beside a window)
+ */
+typedef struct {
+  float scale;           /* > 0 */
+  float softcap;         /* >= 0; 0: none */
+  int32_t window;        /* >= 0; 0: none */
+  const float* slopes;   /* device [heads], or NULL */
+  const int32_t* first;  /* device [n_rows], or NULL: 0 */
+  const int32_t* prefix; /* device [num_seqs], or NULL: 0 */
+} csa_kv8_mask;
+
+/*
+ * csa_kv8_attn -- attention of a step's rows over a csa_kv8 cache that holds the
+ * tokens of their requests, the step's own included (csa_kv8_store runs before).
+ * Query head h reads key head h / (heads / kv_heads).  Requests may have one row
+ * or thousands, in any mix.
+ *   out[r][h] = sum_t softmax_t(a) * v_t,  lse[r][h] = ln sum_t exp(a)
+ * A row that sees no key gets zeros, and an lse of -infinity.  Rows behind the last
+ * request (r >= row_start[num_seqs]) are left as they were.
+ *   q    [n_rows][heads][dim] q_dtype (F32 or BF16), rows q_stride elements apart
+ *   out  [n_rows][heads][dim] out_dtype (F32 or BF16); lse [n_rows][heads] float or NULL
+ *   heads a multiple of kv_heads; max_new >= every request's rows
+ *   row_start, cached as in csa_kv8_store
+ *   ws   at least csa_kv8_attn_workspace_size(...) bytes, 16-byte aligned.  Scratch:
+ *        nothing needs to start at zero, and calls that can overlap need their own.
+ * Probabilities are rounded to fp16 before they meet the values when q and out are
+ * BF16 and dim is 64 or 128; otherwise everything stays in fp32.
+ * A request with more than max_new rows, or out of bounds as in csa_kv8_store, is
+ * skipped; keys in unmapped blocks are skipped (CSA_ERR_DEVICE_BOUNDS).
+ */
+CSA_API int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_rows, int32_t heads,
+                         const int32_t* row_start, const int32_t* cached, int32_t max_new,
+                         const csa_kv8* cache, const csa_block_table* bt, const csa_kv8_mask* mask,
+                         void* out, int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, int32_t* err,
+                         csa_stream_t stream);
+CSA_API size_t csa_kv8_attn_workspace_size(int32_t n_rows, int32_t num_seqs, int32_t heads,
+                                           const csa_kv8* cache, int32_t max_new);
 
 /* Copy the device error word to the host (synchronises `stream`); if `reset`, zero it
  * afterwards.  Returns the recorded csa_status (CSA_OK if none) or CSA_ERR_CUDA. */
