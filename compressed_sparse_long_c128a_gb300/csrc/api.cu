@@ -43,6 +43,12 @@ int check_kv8(const csa_kv8* c) {
   return CSA_OK;
 }
 
+// Query columns of a tile of the few-row kernel: what a request of max_new rows has, up to 32.
+int32_t kv8_cols(int32_t group, int32_t max_new) {
+  const int64_t c = (int64_t)group * max_new;
+  return c > 32 ? 32 : (int32_t)c;
+}
+
 int check_bt(const csa_block_table* bt) {
   if (!bt || !bt->table || bt->num_seqs <= 0 || bt->stride <= 0) return CSA_ERR_INVALID_ARG;
   return CSA_OK;
@@ -430,8 +436,13 @@ size_t csa_kv8_attn_workspace_size(int32_t n_rows, int32_t num_seqs, int32_t hea
                                    int32_t max_new) {
   if (!cache || n_rows <= 0 || num_seqs <= 0 || heads <= 0 || cache->kv_heads <= 0 || cache->dim <= 0 || max_new <= 0)
     return 0;
-  return align_up(
-      kv8_simt_workspace(n_rows, heads, cache->dim, kv8_simt_splits(n_rows, heads, cache->kv_heads)));
+  // the query type decides between the kernels; size for the larger
+  const size_t simt =
+      kv8_simt_workspace(n_rows, heads, cache->dim, kv8_simt_splits(n_rows, heads, cache->kv_heads));
+  const size_t tc = kv8_decode_eligible(CSA_BF16, CSA_BF16, cache->dim)
+                        ? kv8_decode_workspace(cache->dim, kv8_cols(heads / cache->kv_heads, max_new))
+                        : 0;
+  return align_up(simt > tc ? simt : tc);
 }
 
 int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_rows, int32_t heads,
@@ -471,10 +482,18 @@ int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_row
   a.out = out;
   a.out_dtype = out_dtype;
   a.lse = lse;
+  a.err = err;
+  if (kv8_decode_eligible(q_dtype, out_dtype, cache->dim)) {
+    a.q_vec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_stride % 8 == 0;
+    a.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    a.cols = kv8_cols(a.group, max_new);
+    a.few_cols = INT32_MAX;
+    kv8_decode_parts(a, ws);
+    return cuda_status(launch_kv8_decode(a, stream));
+  }
   a.n_splits = kv8_simt_splits(n_rows, heads, cache->kv_heads);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = a.part_o + (size_t)n_rows * heads * a.n_splits * cache->dim;
-  a.err = err;
   return cuda_status(launch_kv8_attn_simt(a, stream));
 }
 

@@ -314,12 +314,21 @@ struct Kv8AttnArgs {
   float* lse;
   float* part_o;  // partial results, see the kernels
   float* part_ml;
+  int32_t* part_head;
   int32_t n_splits;
+  int32_t cols;      // query columns (rows x group) of a tile of the few-row kernel
+  int32_t few_cols;  // it takes the requests of at most so many columns
+  int32_t q_vec, out_vec;  // q rows and out may be accessed 16 bytes at a time
   int32_t* err;
 };
 // CUDA-core kernel, any type and dim: splits of a row's keys, and its scratch
 int32_t kv8_simt_splits(int32_t n_rows, int32_t heads, int32_t kv_heads);
 size_t kv8_simt_workspace(int32_t n_rows, int32_t heads, int32_t dim, int32_t n_splits);
 cudaError_t launch_kv8_attn_simt(const Kv8AttnArgs& a, cudaStream_t s);
+// few rows a request, bf16 queries, dims 64, 128, 256 (k_kv8_decode.cu)
+bool kv8_decode_eligible(int32_t q_dtype, int32_t out_dtype, int32_t dim);
+size_t kv8_decode_workspace(int32_t dim, int32_t cols);
+void kv8_decode_parts(Kv8AttnArgs& a, void* ws);  // the workspace's parts, for a.cols columns
+cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t s);
 
 }  // namespace csa

@@ -52,4 +52,48 @@ __device__ __forceinline__ int warp_last_le(int n, int64_t x, F key) {
   return lo;
 }
 
+// Tiles of T tokens that some row of a request sees: those of the prefix, [tA, tA + nA),
+// then those that causality and the window leave and that are not among them, [tB, tB + nB).
+struct Kv8Tiles {
+  int32_t tA, nA, tB, nB;
+  __device__ __forceinline__ int32_t count() const { return nA + nB; }
+  __device__ __forceinline__ int32_t at(int32_t i) const { return i < nA ? tA + i : tB + i - nA; }
+};
+
+// For keys t with first <= t and (t < pre or lo <= t <= hi), hi < n.
+__device__ __forceinline__ Kv8Tiles kv8_tiles(int32_t T, int32_t first, int32_t pre, int32_t lo, int32_t hi) {
+  Kv8Tiles x;
+  x.tA = first / T;
+  x.nA = first < pre ? (pre + T - 1) / T - x.tA : 0;
+  x.tB = x.nA ? max(lo / T, x.tA + x.nA) : lo / T;
+  x.nB = lo <= hi ? max(0, hi / T + 1 - x.tB) : 0;
+  return x;
+}
+
+// Four e4m3 codes to two f16 pairs (of the low and the high 16 bits of w), exactly.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The power of two at or below x (x >= 0), kept where its reciprocal is a normal number too.
+__device__ __forceinline__ float pow2_floor(float x) {
+  const uint32_t e = min(max(__float_as_uint(x) >> 23, 1u), 253u);
+  return __uint_as_float(e << 23);
+}
+__device__ __forceinline__ float pow2_recip(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+
+// tanh(x) = sign(x) (1 - 2 / (e^(2|x|) + 1)): about 2e-7 off, absolutely.
+__device__ __forceinline__ float tanh_exp(float x) {
+  const float e = fast_exp2(fabsf(x) * 2.885390081777927f);  // 2 log2(e)
+  return copysignf(1.0f - __fdividef(2.0f, e + 1.0f), x);
+}
+
 }  // namespace csa

@@ -426,7 +426,7 @@ typedef struct {
  *   ws   at least csa_kv8_attn_workspace_size(...) bytes, 16-byte aligned.  Scratch:
  *        nothing needs to start at zero, and calls that can overlap need their own.
  * Probabilities are rounded to fp16 before they meet the values when q and out are
- * BF16 and dim is 64 or 128; otherwise everything stays in fp32.
+ * BF16 and dim is 64, 128 or 256; otherwise everything stays in fp32.
  * A request with more than max_new rows, or out of bounds as in csa_kv8_store, is
  * skipped; keys in unmapped blocks are skipped (CSA_ERR_DEVICE_BOUNDS).
  */
