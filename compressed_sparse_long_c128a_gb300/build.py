@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libcsa.so")
 
 SOURCES = ["api.cu", "k_compress.cu", "k_store.cu", "k_indexer.cu", "k_topk.cu", "k_attn.cu", "k_attn_tc.cu",
            "k_indexer_tc.cu", "noalloc.cu", "k_plan.cu", "k_kv8_store.cu", "k_kv8_attn.cu",
-           "k_kv8_decode.cu"]
+           "k_kv8_decode.cu", "k_kv8_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          f"-I{INCLUDE}", f"-I{CSRC}"]

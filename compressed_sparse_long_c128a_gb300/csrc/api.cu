@@ -43,10 +43,23 @@ int check_kv8(const csa_kv8* c) {
   return CSA_OK;
 }
 
-// Query columns of a tile of the few-row kernel: what a request of max_new rows has, up to 32.
-int32_t kv8_cols(int32_t group, int32_t max_new) {
-  const int64_t c = (int64_t)group * max_new;
-  return c > 32 ? 32 : (int32_t)c;
+// How a call is shared between the two tensor-core kernels: columns (rows x group) of a
+// tile of the few-row kernel, the most columns of a request that it takes, and whether
+// the many-row kernel runs too.
+struct Kv8Plan {
+  int32_t cols, few_cols;
+  bool many;
+};
+Kv8Plan kv8_plan(int32_t n_rows, int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t dim, int32_t max_new) {
+  const int32_t group = heads / kv_heads;
+  const int64_t most = (int64_t)group * max_new;
+  Kv8Plan p{most > 32 ? 32 : (int32_t)most, INT32_MAX, false};
+  if (most <= 32 || !kv8_prefill_eligible(dim, group)) return p;
+  // requests of single tokens among long ones keep tiles of their own width
+  p.many = true;
+  p.few_cols = 32;
+  p.cols = group > 32 ? 32 : group;
+  return p;
 }
 
 int check_bt(const csa_block_table* bt) {
@@ -440,7 +453,9 @@ size_t csa_kv8_attn_workspace_size(int32_t n_rows, int32_t num_seqs, int32_t hea
   const size_t simt =
       kv8_simt_workspace(n_rows, heads, cache->dim, kv8_simt_splits(n_rows, heads, cache->kv_heads));
   const size_t tc = kv8_decode_eligible(CSA_BF16, CSA_BF16, cache->dim)
-                        ? kv8_decode_workspace(cache->dim, kv8_cols(heads / cache->kv_heads, max_new))
+                        ? kv8_decode_workspace(
+                              cache->dim,
+                              kv8_plan(n_rows, num_seqs, heads, cache->kv_heads, cache->dim, max_new).cols)
                         : 0;
   return align_up(simt > tc ? simt : tc);
 }
@@ -486,10 +501,12 @@ int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_row
   if (kv8_decode_eligible(q_dtype, out_dtype, cache->dim)) {
     a.q_vec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_stride % 8 == 0;
     a.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    a.cols = kv8_cols(a.group, max_new);
-    a.few_cols = INT32_MAX;
+    const Kv8Plan p = kv8_plan(n_rows, bt->num_seqs, heads, cache->kv_heads, cache->dim, max_new);
+    a.cols = p.cols;
+    a.few_cols = p.few_cols;
     kv8_decode_parts(a, ws);
-    return cuda_status(launch_kv8_decode(a, stream));
+    if (launch_kv8_decode(a, stream) != cudaSuccess) return CSA_ERR_CUDA;
+    return p.many ? cuda_status(launch_kv8_prefill(a, stream)) : CSA_OK;
   }
   a.n_splits = kv8_simt_splits(n_rows, heads, cache->kv_heads);
   a.part_o = reinterpret_cast<float*>(ws);

@@ -330,5 +330,8 @@ bool kv8_decode_eligible(int32_t q_dtype, int32_t out_dtype, int32_t dim);
 size_t kv8_decode_workspace(int32_t dim, int32_t cols);
 void kv8_decode_parts(Kv8AttnArgs& a, void* ws);  // the workspace's parts, for a.cols columns
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t s);
+// many rows a request: those of more than few_cols columns (k_kv8_prefill.cu)
+bool kv8_prefill_eligible(int32_t dim, int32_t group);
+cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s);
 
 }  // namespace csa
