@@ -17,9 +17,11 @@
 //    and go to the swizzled operand tiles, two stages of keys and of values.  Both query
 //    tiles use each converted tile.
 //  * Softmax: warps 0-3 hold the rows of tile 0, warps 4-7 those of tile 1, a thread a row,
-//    so that no value crosses lanes.  The scores are read twice, 32 columns at a time (once
-//    for the maximum), since 128 of them would not fit the registers.  The row's maximum is
-//    raised, and O rescaled, only when a score passes it by 2^8.  Scales are those of 16
+//    so that no value crosses lanes.  The scores are read twice, 64 columns at a time (once
+//    for the maximum), since 128 of them do not fit the registers.  Caps and biases are
+//    compiled apart: with their code in the common loop, waiting for instructions cost more
+//    than half of the time.  The row's
+//    maximum is raised, and O rescaled, only when a score passes it by 2^8.  Scales are those of 16
 //    tokens: the key's multiplies the scores, the value's, relative to the largest that the
 //    CTA's rows see, enters the exponent, P = 2^(s - m + 7 + log2(v / v_max)), and is
 //    divided out of each 16 columns' part of the sum.
@@ -39,8 +41,9 @@ constexpr int kTile = 128;     // keys of a tile
 constexpr int kM = 128;        // rows of a query tile
 constexpr int kMTiles = 2;
 constexpr int kSoftmax = kMTiles * 128, kConvert = 128;
-constexpr int kThreads = kSoftmax + kConvert + 32;
-constexpr int kMmaWarp = kThreads / 32 - 1;
+constexpr int kThreads = kSoftmax + kConvert + 32;  // the last warp issues the products
+constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
+constexpr int kHalf = kTile / 2;  // columns of a tile that a softmax thread holds at a time
 constexpr int kGroups = kTile / 16;  // tokens that share a scale
 constexpr int kScaleBufs = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -93,20 +96,22 @@ struct Part {
 
 // ------------------------------------------------------------------ conversion
 
+// Thread ct takes piece ct % CH of rows ct / CH + i kConvert / CH (CH pieces of 16 dims a row).
 template <int D>
 __device__ __forceinline__ void load_units(const Kv8AttnArgs& a, const Part& w, const uint8_t* codes, int t, int ct,
                                            uint4* x) {
   constexpr int CH = D / 16;
-  const int P = a.cache.rows_per_block, base = w.tiles.at(t) * kTile;
+  const int P = a.cache.rows_per_block;
+  const int tok0 = w.tiles.at(t) * kTile + ct / CH;
+  const uint8_t* mine = codes + (int64_t)w.kvh * P * D + (ct % CH) * 16;
 #pragma unroll
   for (int i = 0; i < Cfg<D>::kUnits; ++i) {
-    const int u = ct + i * kConvert, tok = base + u / CH;
+    const int tok = tok0 + i * (kConvert / CH);
     x[i] = make_uint4(0, 0, 0, 0);
     if (tok < w.n) {
       const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok / P);
       if (blk >= 0)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(
-            codes + (((int64_t)blk * a.cache.kv_heads + w.kvh) * P + (tok & (P - 1))) * D + (u % CH) * 16));
+        x[i] = __ldg(reinterpret_cast<const uint4*>(mine + ((int64_t)blk * a.cache.kv_heads * P + (tok & (P - 1))) * D));
     }
   }
 }
@@ -114,20 +119,21 @@ __device__ __forceinline__ void load_units(const Kv8AttnArgs& a, const Part& w, 
 template <int D>
 __device__ __forceinline__ void store_units(uint8_t* tile, int ct, const uint4* x) {
   constexpr int CH = D / 16;
+  const int r = ct / CH, c = ct % CH;
+  // the pieces of a row are written together: those of its second half begin with their
+  // upper 8 dims, so that no two fall on one bank
+  const bool swap = c & 4;
+  uint8_t* at0 = tile + sw128_offset(r, 16 * c + (swap ? 8 : 0), kTile);
+  uint8_t* at1 = tile + sw128_offset(r, 16 * c + (swap ? 0 : 8), kTile);
 #pragma unroll
-  for (int i = 0; i < Cfg<D>::kUnits; ++i) {
-    const int u = ct + i * kConvert, r = u / CH, c = u % CH;
+  for (int i = 0; i < Cfg<D>::kUnits; ++i) {  // rows a multiple of 8 apart: the swizzle stays
     uint4 lo, hi;
     e4m3x4_to_f16x2(x[i].x, lo.x, lo.y);
     e4m3x4_to_f16x2(x[i].y, lo.z, lo.w);
     e4m3x4_to_f16x2(x[i].z, hi.x, hi.y);
     e4m3x4_to_f16x2(x[i].w, hi.z, hi.w);
-    // the eight pieces of a row are written together: those of the second half of the dims
-    // begin with their upper half, so that no two fall on one bank
-    const bool swap = c & 4;
-    const uint32_t k = 16 * c;
-    *reinterpret_cast<uint4*>(tile + sw128_offset(r, k + (swap ? 8 : 0), kTile)) = swap ? hi : lo;
-    *reinterpret_cast<uint4*>(tile + sw128_offset(r, k + (swap ? 0 : 8), kTile)) = swap ? lo : hi;
+    *reinterpret_cast<uint4*>(at0 + i * (kConvert / CH) * 128) = swap ? hi : lo;
+    *reinterpret_cast<uint4*>(at1 + i * (kConvert / CH) * 128) = swap ? lo : hi;
   }
 }
 
@@ -252,8 +258,8 @@ __device__ void mma_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Mis
 
 // ------------------------------------------------------------------ softmax
 
-template <int D>
-__device__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem, int st) {
+template <int D, bool CAP, bool BIAS>
+__device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem, int st) {
   using C = Cfg<D>;
   const int i = st >> 7, m_row = st & 127, G = a.group;
   const int tok = w.i0 + i * w.tpt + m_row / G, head = w.kvh * G + m_row % G;
@@ -298,10 +304,9 @@ __device__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
     mbar_arrive(&ms.q_full);
   }
 
-  const bool cap = a.mask.softcap > 0.f, bias = a.mask.slopes != nullptr;
-  const float fac = p2 * a.mask.scale * (cap ? 1.0f / a.mask.softcap : kLog2e);
+  const float fac = p2 * a.mask.scale * (CAP ? 1.0f / a.mask.softcap : kLog2e);
   const float post = a.mask.softcap * kLog2e;
-  const float slope = bias && real ? a.mask.slopes[head] * kLog2e : 0.f;
+  const float slope = BIAS && real ? a.mask.slopes[head] * kLog2e : 0.f;
   // rows that do not exist see every key, so that they ask for no mask
   const int p = real ? w.r.cached + tok : INT32_MAX;
   const int first = real && a.mask.first ? max(0, a.mask.first[row]) : 0;
@@ -313,34 +318,42 @@ __device__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   for (int t = 0; t < w.count; ++t) {
     const int sb = t % kScaleBufs, t0 = w.tiles.at(t) * kTile;
     wait_or_abort(ms, &ms.sc_full[sb], (t / kScaleBufs) & 1, a.err);
-    const bool whole = t0 >= first && t0 + kTile <= w.n && ((t0 >= lo && t0 + kTile - 1 <= p) || t0 + kTile <= w.pre);
     bool mapped = true;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) mapped &= ms.ks[sb][g] >= 0.f;
+    const bool whole = t0 >= first && t0 + kTile <= w.n && ((t0 >= lo && t0 + kTile - 1 <= p) || t0 + kTile <= w.pre);
     const bool plain = __all_sync(0xffffffffu, whole && mapped);
     wait_or_abort(ms, &ms.s_full[i], t & 1, a.err);
     tc_fence_after();
-
-    // scores of 16 columns in log2 units, from the accumulator; -inf where the row does not see the key
-    auto finish = [&](float* x, int g) {
-      const float f = fac * fabsf(ms.ks[sb][g]);
+    float x[kHalf];
+    auto load = [&](int h) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] *= f;
-      if (cap) {
+      for (int c = 0; c < kHalf; c += 16) tmem_ld16(s_addr + kHalf * h + c, x + c);
+      tmem_wait_ld();
+    };
+    // what turns the accumulator's 16 columns into scores in log2 units, before the cap; not 0, so
+    // that it leaves -inf alone
+    auto factor = [&](int h, int j) { return fmaxf(fac * ms.ks[sb][h * (kHalf / 16) + j], FLT_MIN); };
+    auto finish = [&](int h) {
+      if constexpr (CAP || BIAS) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = post * tanh_exp(x[k]);
-      }
-      if (bias) {
-        const float d0 = (float)(p - (t0 + 16 * g));
+        for (int j = 0; j < kHalf / 16; ++j) {
+          const float f = factor(h, j);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] -= slope * fabsf(d0 - (float)k);
+          for (int k = 16 * j; k < 16 * j + 16; ++k) {
+            float y = x[k] * f;
+            if constexpr (CAP) y = post * tanh_exp(y);
+            if constexpr (BIAS) y -= slope * fabsf((float)(p - t0 - kHalf * h) - (float)k);
+            x[k] = y;
+          }
+        }
       }
       if (!plain) {
-        const bool no_block = ms.ks[sb][g] < 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int key = t0 + 16 * g + k;
-          const bool see = key < w.n && key >= first && (key < w.pre || (key <= p && key >= lo)) && !no_block;
+        for (int k = 0; k < kHalf; ++k) {
+          const int key = t0 + kHalf * h + k;
+          const bool see = key < w.n && key >= first && (key < w.pre || (key <= p && key >= lo)) &&
+                           ms.ks[sb][h * (kHalf / 16) + k / 16] >= 0.f;
           x[k] = see ? x[k] : -INFINITY;
         }
       }
@@ -348,27 +361,20 @@ __device__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
 
     // ---- the tile's maximum
     float mt = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      load(h);
+      // the cap rises with the accumulator: without a bias or a mask only the maximum is capped
+      const bool raw = CAP && !BIAS && plain;
+      if (!raw) finish(h);
 #pragma unroll
-    for (int g = 0; g < kGroups; g += 2) {
-      float x[32];
-      tmem_ld16(s_addr + 16 * g, x);
-      tmem_ld16(s_addr + 16 * g + 16, x + 16);
-      tmem_wait_ld();
+      for (int j = 0; j < kHalf / 16; ++j) {
+        float z = x[16 * j];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float* y = x + 16 * j;
-        if (bias || !plain) {
-          finish(y, g + j);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) mt = fmaxf(mt, y[k]);
-        } else {  // rising in the accumulator: only its maximum is finished
-          float z = y[0];
-#pragma unroll
-          for (int k = 1; k < 16; ++k) z = fmaxf(z, y[k]);
-          z *= fac * ms.ks[sb][g + j];
-          if (cap) z = post * tanh_exp(z);
-          mt = fmaxf(mt, z);
-        }
+        for (int k = 1; k < 16; ++k) z = fmaxf(z, x[16 * j + k]);
+        if (raw) z = post * tanh_exp(z * factor(h, j));
+        else if (!CAP && !BIAS) z *= factor(h, j);
+        mt = fmaxf(mt, z);
       }
     }
     if (__any_sync(0xffffffffu, mt > m + kRescaleMargin)) {
@@ -379,48 +385,41 @@ __device__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
         // O holds exactly the tiles before t once O(t-1) is complete
         wait_or_abort(ms, &ms.o_done[i], (t - 1) & 1, a.err);
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          float o[16];
-          tmem_ld16(o_addr + 16 * c, o);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld16(o_addr + c, o);
+          tmem_ld16(o_addr + c + 16, o + 16);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] *= alpha;
-          tmem_st16(o_addr + 16 * c, o);
+          for (int k = 0; k < 32; ++k) o[k] *= alpha;
+          tmem_st16(o_addr + c, o);
+          tmem_st16(o_addr + c + 16, o + 16);
         }
       }
     }
-    // ---- P over S
+    // ---- P over S: the first half's 32 columns end before the second half's scores begin
     const float shift = kPShift - m;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      load(h);
+      finish(h);
 #pragma unroll
-    for (int g = 0; g < kGroups; g += 2) {
-      float x[32];
-      tmem_ld16(s_addr + 16 * g, x);
-      tmem_ld16(s_addr + 16 * g + 16, x + 16);
-      tmem_wait_ld();
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float* y = x + 16 * j;
-        const float add = shift + ms.lv[sb][g + j];
-        if (cap || bias || !plain) {
-          finish(y, g + j);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) y[k] = fast_exp2(y[k] + add);
-        } else {
-          const float f = fac * ms.ks[sb][g + j];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) y[k] = fast_exp2(fmaf(y[k], f, add));
-        }
+      for (int j = 0; j < kHalf / 16; ++j) {
+        const float f = factor(h, j), add = shift + ms.lv[sb][h * (kHalf / 16) + j];
         float s0 = 0.f, s1 = 0.f;
         uint32_t pw[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          s0 += y[2 * k];
-          s1 += y[2 * k + 1];
-          pw[k] = f32x2_to_f16x2(y[2 * k], y[2 * k + 1]);
+          const float x0 = x[16 * j + 2 * k], x1 = x[16 * j + 2 * k + 1];
+          const float y0 = fast_exp2(CAP || BIAS ? x0 + add : fmaf(x0, f, add));
+          const float y1 = fast_exp2(CAP || BIAS ? x1 + add : fmaf(x1, f, add));
+          s0 += y0;
+          s1 += y1;
+          pw[k] = f32x2_to_f16x2(y0, y1);
         }
-        l = fmaf(s0 + s1, ms.rv[sb][g + j], l);
-        tmem_st8(s_addr + 8 * (g + j), pw);
+        l = fmaf(s0 + s1, ms.rv[sb][h * (kHalf / 16) + j], l);
+        tmem_st8(s_addr + 32 * h + 8 * j, pw);
       }
     }
     tmem_wait_st();
@@ -456,7 +455,7 @@ __device__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   tc_fence_before();
 }
 
-template <int D>
+template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t raw[];
@@ -522,11 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
   if (tid < kSoftmax) {
-    softmax_role<D>(a, w, smem, ms, tmem, tid);
-  } else if (tid < kSoftmax + kConvert) {
-    convert_role<D>(a, w, smem, ms, tid - kSoftmax);
+    softmax_role<D, CAP, BIAS>(a, w, smem, ms, tmem, tid);
   } else {
-    if ((tid & 31) == 0) mma_role<D>(a, w, smem, ms, tmem);
+    if (tid < kSoftmax + kConvert) convert_role<D>(a, w, smem, ms, tid - kSoftmax);
+    else if (tid == kSoftmax + kConvert) mma_role<D>(a, w, smem, ms, tmem);
     __syncwarp();
   }
   __syncthreads();
@@ -534,19 +532,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
   if (wid == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, bool CAP, bool BIAS>
 cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t s) {
   static PerDevice attr;
   const cudaError_t e = with_device_slot(attr, [](int, int64_t& v) {
     if (v) return cudaSuccess;
-    const cudaError_t err =
-        cudaFuncSetAttribute(kv8_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+    const cudaError_t err = cudaFuncSetAttribute(kv8_prefill_kernel<D, CAP, BIAS>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
     if (err == cudaSuccess) v = 1;
     return err;
   });
   if (e != cudaSuccess) return e;
   const unsigned gx = (unsigned)(a.n_rows / (kMTiles * (kM / a.group)) + a.bt.num_seqs);
-  return launch_k(kv8_prefill_kernel<D>, dim3(gx, a.cache.kv_heads), dim3(kThreads), smem_bytes<D>(), s, 0, a);
+  return launch_k(kv8_prefill_kernel<D, CAP, BIAS>, dim3(gx, a.cache.kv_heads), dim3(kThreads), smem_bytes<D>(), s, 0,
+                  a);
+}
+
+template <int D>
+cudaError_t launch_dim(const Kv8AttnArgs& a, cudaStream_t s) {
+  const bool cap = a.mask.softcap > 0.f, bias = a.mask.slopes != nullptr;
+  if (cap) return bias ? launch<D, true, true>(a, s) : launch<D, true, false>(a, s);
+  return bias ? launch<D, false, true>(a, s) : launch<D, false, false>(a, s);
 }
 
 }  // namespace
@@ -554,7 +560,7 @@ cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t s) {
 bool kv8_prefill_eligible(int32_t dim, int32_t group) { return (dim == 64 || dim == 128) && group <= kM; }
 
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s) {
-  return a.cache.dim == 64 ? launch<64>(a, s) : launch<128>(a, s);
+  return a.cache.dim == 64 ? launch_dim<64>(a, s) : launch_dim<128>(a, s);
 }
 
 }  // namespace csa
