@@ -43,9 +43,9 @@ constexpr int kMTiles = 2;
 constexpr int kSoftmax = kMTiles * 128, kConvert = 128;
 constexpr int kThreads = kSoftmax + kConvert + 32;  // the last warp issues the products
 constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
-constexpr int kHalf = kTile / 2;  // columns of a tile that a softmax thread holds at a time
+constexpr int kHalf = kTile / 4;  // columns of a tile that a softmax thread holds at a time
 constexpr int kGroups = kTile / 16;  // tokens that share a scale
-constexpr int kScaleBufs = 4;
+constexpr int kScaleBufs = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleMargin = 8.0f, kPShift = 7.0f;
 
@@ -67,8 +67,9 @@ struct Misc {
   int32_t owner;
   float red[kConvert / 32];
   float v_max;
-  // by tile mod 4 and 16 tokens: key scale (negative: no block), log2 of the value scale
+  // by tile mod 8 and 16 tokens: offset of the codes (-1: none), key scale (negative: no block), log2 of the value scale
   // relative to v_max, and its inverse
+  int64_t src[kScaleBufs][kGroups];
   alignas(16) float ks[kScaleBufs][kGroups], lv[kScaleBufs][kGroups], rv[kScaleBufs][kGroups];
 };
 
@@ -96,44 +97,48 @@ struct Part {
 
 // ------------------------------------------------------------------ conversion
 
-// Thread ct takes piece ct % CH of rows ct / CH + i kConvert / CH (CH pieces of 16 dims a row).
+// Eight neighbouring lanes take four pieces (16 dims) of two rows: what they write to the
+// swizzled tile together falls on different banks.
 template <int D>
-__device__ __forceinline__ void load_units(const Kv8AttnArgs& a, const Part& w, const uint8_t* codes, int t, int ct,
-                                           uint4* x) {
-  constexpr int CH = D / 16;
-  const int P = a.cache.rows_per_block;
-  const int tok0 = w.tiles.at(t) * kTile + ct / CH;
-  const uint8_t* mine = codes + (int64_t)w.kvh * P * D + (ct % CH) * 16;
+struct Unit {
+  int row, piece;  // row: of the thread's first unit, the others kConvert 16 / D further each
+  __device__ __forceinline__ explicit Unit(int ct) {
+    if constexpr (D == 64) {
+      row = ct >> 2, piece = ct & 3;
+    } else {
+      row = ((ct >> 2) & 1) + 2 * (ct >> 4), piece = (ct & 3) + ((ct >> 1) & 4);
+    }
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void load_units(const int64_t* src, const uint8_t* codes, const Unit<D>& un, uint4* x) {
+  constexpr int kRows = kConvert / (D / 16);
 #pragma unroll
   for (int i = 0; i < Cfg<D>::kUnits; ++i) {
-    const int tok = tok0 + i * (kConvert / CH);
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (tok < w.n) {
-      const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok / P);
-      if (blk >= 0)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(mine + ((int64_t)blk * a.cache.kv_heads * P + (tok & (P - 1))) * D));
-    }
+    const int row = un.row + i * kRows;
+    const int64_t at = src[row / 16];  // tokens past the sequence hold some code: only V needs zeros there
+    x[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at + (row % 16) * D + un.piece * 16))
+                   : make_uint4(0, 0, 0, 0);
   }
 }
 
+// `left`: rows of the tile that hold tokens; the others become zeros
 template <int D>
-__device__ __forceinline__ void store_units(uint8_t* tile, int ct, const uint4* x) {
-  constexpr int CH = D / 16;
-  const int r = ct / CH, c = ct % CH;
-  // the pieces of a row are written together: those of its second half begin with their
-  // upper 8 dims, so that no two fall on one bank
-  const bool swap = c & 4;
-  uint8_t* at0 = tile + sw128_offset(r, 16 * c + (swap ? 8 : 0), kTile);
-  uint8_t* at1 = tile + sw128_offset(r, 16 * c + (swap ? 0 : 8), kTile);
+__device__ __forceinline__ void store_units(uint8_t* tile, const Unit<D>& un, const uint4* x, int left) {
+  constexpr int kRows = kConvert / (D / 16);
+  uint8_t* at0 = tile + sw128_offset(un.row, 16 * un.piece, kTile);
+  uint8_t* at1 = tile + sw128_offset(un.row, 16 * un.piece + 8, kTile);
 #pragma unroll
   for (int i = 0; i < Cfg<D>::kUnits; ++i) {  // rows a multiple of 8 apart: the swizzle stays
     uint4 lo, hi;
-    e4m3x4_to_f16x2(x[i].x, lo.x, lo.y);
-    e4m3x4_to_f16x2(x[i].y, lo.z, lo.w);
-    e4m3x4_to_f16x2(x[i].z, hi.x, hi.y);
-    e4m3x4_to_f16x2(x[i].w, hi.z, hi.w);
-    *reinterpret_cast<uint4*>(at0 + i * (kConvert / CH) * 128) = swap ? hi : lo;
-    *reinterpret_cast<uint4*>(at1 + i * (kConvert / CH) * 128) = swap ? lo : hi;
+    const bool there = un.row + i * kRows < left;
+    e4m3x4_to_f16x2(there ? x[i].x : 0u, lo.x, lo.y);
+    e4m3x4_to_f16x2(there ? x[i].y : 0u, lo.z, lo.w);
+    e4m3x4_to_f16x2(there ? x[i].z : 0u, hi.x, hi.y);
+    e4m3x4_to_f16x2(there ? x[i].w : 0u, hi.z, hi.w);
+    *reinterpret_cast<uint4*>(at0 + i * kRows * 128) = lo;
+    *reinterpret_cast<uint4*>(at1 + i * kRows * 128) = hi;
   }
 }
 
@@ -142,19 +147,15 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   using C = Cfg<D>;
   const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.cache.k);
   const uint8_t* vc = reinterpret_cast<const uint8_t*>(a.cache.v);
-  const int P = a.cache.rows_per_block, Hk = a.cache.kv_heads;
-  uint4 kx[C::kUnits], vx[C::kUnits];
-  if (w.count > 0) {
-    load_units<D>(a, w, kc, 0, ct, kx);
-    load_units<D>(a, w, vc, 0, ct, vx);
-  }
+  const int P = a.cache.rows_per_block, Hk = a.cache.kv_heads, shift = 31 - __clz(P);
   // the largest value scale of the blocks that the tiles touch
   float top = kKv8MinScale;
   for (int part = 0; part < 2; ++part) {
     const int t0 = (part ? w.tiles.tB : w.tiles.tA) * kTile, nt = part ? w.tiles.nB : w.tiles.nA;
-    const int lb1 = (min(w.n, t0 + nt * kTile) + P - 1) / P;
+    const int lb1 = (min(w.n, t0 + nt * kTile) + P - 1) >> shift;
     if (nt > 0)
-      for (int lb = t0 / P + ct; lb < lb1; lb += kConvert) {
+#pragma unroll 4
+      for (int lb = (t0 >> shift) + ct; lb < lb1; lb += kConvert) {
         const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, lb);
         if (blk >= 0) top = fmaxf(top, a.cache.v_scale[(int64_t)blk * Hk + w.kvh]);
       }
@@ -166,39 +167,60 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   for (int i = 0; i < kConvert / 32; ++i) top = fmaxf(top, ms.red[i]);
   if (ct == 0) ms.v_max = top;  // read by the softmax after sc_full, or after the CTA's last barrier
   const float inv_top = 1.0f / top;
-  for (int t = 0; t < w.count; ++t) {
-    const int st = t & 1;
-    const uint32_t prev = ((t >> 1) & 1) ^ 1;  // the use of the stage before this one
-    if (ct < 32) {
-      if (ct < kGroups) {
-        const int tok = w.tiles.at(t) * kTile + 16 * ct;
-        float ks = -1.f, vs = 1.f;
-        if (tok < w.n) {
-          const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok / P);
-          if (blk >= 0) {
-            ks = a.cache.k_scale[(int64_t)blk * Hk + w.kvh];
-            vs = fmaxf(a.cache.v_scale[(int64_t)blk * Hk + w.kvh] * inv_top, kKv8MinScale);
-          } else {
-            record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
-          }
+
+  // where the tile's tokens are, and their scales, 16 tokens a lane of the first warp
+  auto look_up = [&](int t) {
+    if (ct >= 32 || t >= w.count) return;
+    const int sb = t % kScaleBufs;
+    if (ct < kGroups) {
+      const int tok = w.tiles.at(t) * kTile + 16 * ct;
+      float ks = -1.f, vs = 1.f;
+      int64_t src = -1;
+      if (tok < w.n) {
+        const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok >> shift);
+        if (blk >= 0) {
+          const int64_t at = (int64_t)blk * Hk + w.kvh;
+          src = (at * P + (tok & (P - 1))) * D;
+          ks = a.cache.k_scale[at];
+          vs = fmaxf(a.cache.v_scale[at] * inv_top, kKv8MinScale);
+        } else {
+          record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
         }
-        ms.ks[t % kScaleBufs][ct] = ks;
-        ms.lv[t % kScaleBufs][ct] = log2f(vs);
-        ms.rv[t % kScaleBufs][ct] = 1.0f / vs;
       }
-      __syncwarp();
-      if (ct == 0) mbar_arrive(&ms.sc_full[t % kScaleBufs]);
+      ms.src[sb][ct] = src;
+      ms.ks[sb][ct] = ks;
+      ms.lv[sb][ct] = log2f(vs);
+      ms.rv[sb][ct] = 1.0f / vs;
     }
+    __syncwarp();
+    if (ct == 0) mbar_arrive(&ms.sc_full[sb]);
+  };
+  const Unit<D> un(ct);
+  uint4 kx[C::kUnits], vx[C::kUnits];
+  look_up(0);
+  look_up(1);
+  named_bar(1, kConvert);
+  if (w.count > 0) {
+    load_units<D>(ms.src[0], kc, un, kx);
+    load_units<D>(ms.src[0], vc, un, vx);
+  }
+  for (int t = 0; t < w.count; ++t) {
+    const int st = t & 1, left = w.n - w.tiles.at(t) * kTile;
+    const uint32_t prev = ((t >> 1) & 1) ^ 1;  // the use of the stage before this one
     if (t >= 2) wait_or_abort(ms, &ms.k_free[st], prev, a.err);
-    store_units<D>(smem + C::kOffK + st * C::kTileBytes, ct, kx);
+    store_units<D>(smem + C::kOffK + st * C::kTileBytes, un, kx, left);
     fence_proxy_async();
     mbar_arrive(&ms.k_full[st]);
-    if (t + 1 < w.count) load_units<D>(a, w, kc, t + 1, ct, kx);
+    // tile t - 3 and all before it are done with (v_free, one tile ago): its place takes tile t + 2
+    look_up(t + 2);
+    const int64_t* src = ms.src[(t + 1) % kScaleBufs];
+    if (t + 1 < w.count) load_units<D>(src, kc, un, kx);
     if (t >= 2) wait_or_abort(ms, &ms.v_free[st], prev, a.err);
-    store_units<D>(smem + C::kOffV + st * C::kTileBytes, ct, vx);
+    store_units<D>(smem + C::kOffV + st * C::kTileBytes, un, vx, left);
     fence_proxy_async();
     mbar_arrive(&ms.v_full[st]);
-    if (t + 1 < w.count) load_units<D>(a, w, vc, t + 1, ct, vx);
+    if (t + 1 < w.count) load_units<D>(src, vc, un, vx);
+    named_bar(1, kConvert);  // the next tile's addresses
   }
 }
 
@@ -362,7 +384,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     // ---- the tile's maximum
     float mt = -INFINITY;
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kTile / kHalf; ++h) {
       load(h);
       // the cap rises with the accumulator: without a bias or a mask only the maximum is capped
       const bool raw = CAP && !BIAS && plain;
@@ -401,7 +423,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     // ---- P over S: the first half's 32 columns end before the second half's scores begin
     const float shift = kPShift - m;
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kTile / kHalf; ++h) {
       load(h);
       finish(h);
 #pragma unroll
@@ -419,7 +441,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
           pw[k] = f32x2_to_f16x2(y0, y1);
         }
         l = fmaf(s0 + s1, ms.rv[sb][h * (kHalf / 16) + j], l);
-        tmem_st8(s_addr + 32 * h + 8 * j, pw);
+        tmem_st8(s_addr + kHalf / 2 * h + 8 * j, pw);
       }
     }
     tmem_wait_st();
