@@ -3,25 +3,24 @@
 //
 // 4 D FLOPs a row, head and key: the tensor pipe bounds it.  One CTA an SM takes 256
 // query rows (tokens x query heads of one key head, token-major) as two tiles of M = 128,
-// and walks the keys that its rows see in tiles of 128:
+// and walks the keys that its rows see in tiles of 64:
 //
-//   S_i [128 x 128]  = Q_i [128 x D] . K^T          both operands from shared memory
-//   O_i [128 x D]   += P_i [128 x 128] . V          P from TMEM, where it replaces S_i
+//   S_i [128 x 64]  = Q_i [128 x D] . K^T          both operands from shared memory
+//   O_i [128 x D]  += P_i [128 x 64] . V           P from TMEM, where it replaces S_i
 //
-//  * TMEM: S_0, S_1 (128 columns each), O_0, O_1 (D columns each).  P_i (f16, 64 columns)
-//    is written over S_i.  One thread issues S_0(t), O_1(t-1), S_1(t), O_0(t): while the
-//    softmax works on one tile's scores, the pipe has the other tile's two products.
-//    The pipe executes them in the order of issue, so S_i(t+1) follows O_i(t), which reads
-//    P_i(t), without a wait between them.
-//  * Four warps convert: codes of the next tile wait in registers, become f16 (exactly)
-//    and go to the swizzled operand tiles, two stages of keys and of values.  Both query
+//  * TMEM: S_0 and S_1, two buffers of 64 columns each, O_0, O_1 (D columns each).  P_i (f16,
+//    32 columns) is written over S_i.  One thread issues S_0(t+1), S_1(t+1), O_0(t), O_1(t): the
+//    scores of the next tile are there when the softmax comes to them.  The pipe executes
+//    them in the order of issue, so S_i(t+1) follows O_i(t-1), which reads the P_i(t-1) under it,
+//    without a wait between them.  (With tiles of 128 keys and one S_i, each softmax
+//    waited for two products and their hand-over: 1.65 ms instead of PREFILL_US.)
+//  * Four warps convert: codes of the next two tiles wait in registers, become f16 (exactly)
+//    and go to the swizzled operand tiles, four stages of keys and of values.  Both query
 //    tiles use each converted tile.
 //  * Softmax: warps 0-3 hold the rows of tile 0, warps 4-7 those of tile 1, a thread a row,
-//    so that no value crosses lanes.  The scores are read twice, 64 columns at a time (once
-//    for the maximum), since 128 of them do not fit the registers.  Caps and biases are
-//    compiled apart: with their code in the common loop, waiting for instructions cost more
-//    than half of the time.  The row's
-//    maximum is raised, and O rescaled, only when a score passes it by 2^8.  Scales are those of 16
+//    so that no value crosses lanes.  The maximum is raised, and O rescaled, only when a score
+//    passes it by 2^8.  Caps and biases are compiled apart: with their code in the common
+//    loop, waiting for instructions cost a third of the time.  Scales are those of 16
 //    tokens: the key's multiplies the scores, the value's, relative to the largest that the
 //    CTA's rows see, enters the exponent, P = 2^(s - m + 7 + log2(v / v_max)), and is
 //    divided out of each 16 columns' part of the sum.
@@ -37,48 +36,51 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTile = 128;     // keys of a tile
+constexpr int kTile = 64;      // keys of a tile
 constexpr int kM = 128;        // rows of a query tile
 constexpr int kMTiles = 2;
+constexpr int kStages = 2;     // pairs of key tiles, and of value tiles, in shared memory
 constexpr int kSoftmax = kMTiles * 128, kConvert = 128;
-constexpr int kThreads = kSoftmax + kConvert + 32;  // the last warp issues the products
-constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
-constexpr int kHalf = kTile / 4;  // columns of a tile that a softmax thread holds at a time
+constexpr int kThreads = kSoftmax + kConvert + 64;
+constexpr int kMmaWarp = (kSoftmax + kConvert) / 32, kLookWarp = kMmaWarp + 1;
 constexpr int kGroups = kTile / 16;  // tokens that share a scale
-constexpr int kScaleBufs = 8;
+constexpr int kPairBufs = 8;         // pairs of tiles whose addresses and scales are kept
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleMargin = 8.0f, kPShift = 7.0f;
 
 template <int D>
 struct Cfg {
-  static constexpr uint32_t kAtom = kTile * 128;             // 128 rows of 64 f16
-  static constexpr uint32_t kTileBytes = kAtom * (D / 64);   // a query, key or value tile
-  static constexpr uint32_t kOffK = kMTiles * kTileBytes, kOffV = kOffK + 2 * kTileBytes;
-  static constexpr uint32_t kOffMisc = kOffV + 2 * kTileBytes;
-  static constexpr uint32_t kColS = 0, kColO = kMTiles * kTile;
+  static constexpr uint32_t kQAtom = kM * 128, kAtom = kTile * 128;  // rows of 64 f16
+  static constexpr uint32_t kQBytes = kQAtom * (D / 64), kTileBytes = kAtom * (D / 64);
+  static constexpr uint32_t kOffK = kMTiles * kQBytes, kOffV = kOffK + 2 * kStages * kTileBytes;
+  static constexpr uint32_t kOffMisc = kOffV + 2 * kStages * kTileBytes;
+  static constexpr uint32_t kColO = kMTiles * 2 * kTile;      // S_i(t) at (2 i + t % 2) kTile
   static constexpr int kUnits = kTile * (D / 16) / kConvert;  // 16-byte pieces of a tile a thread
 };
 
 struct Misc {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
-  uint64_t q_full, s_full[kMTiles], p_full[kMTiles], o_done[kMTiles], sc_full[kScaleBufs], mma_done;
+  uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+  // by the parity of t: who waits for a tile may be one tile behind, never two
+  uint64_t s_full[kMTiles][2], p_full[kMTiles][2], o_done[kMTiles][2];
+  uint64_t at_full[kPairBufs], at_free[kPairBufs], q_full, mma_done;
   uint32_t tmem_base;
   int32_t abort;
   int32_t owner;
   float red[kConvert / 32];
   float v_max;
-  // by tile mod 8 and 16 tokens: offset of the codes (-1: none), key scale (negative: no block), log2 of the value scale
-  // relative to v_max, and its inverse
-  int64_t src[kScaleBufs][kGroups];
-  alignas(16) float ks[kScaleBufs][kGroups], lv[kScaleBufs][kGroups], rv[kScaleBufs][kGroups];
+  // of the last tiles, by 16 tokens: offset of the codes (-1: none), key scale (negative: no block),
+  // log2 of the value scale relative to v_max, and its inverse
+  int64_t src[2 * kPairBufs][kGroups];
+  float ks[2 * kPairBufs][kGroups], lv[2 * kPairBufs][kGroups], rv[2 * kPairBufs][kGroups];
 };
 
 template <int D>
 constexpr uint32_t smem_bytes() { return Cfg<D>::kOffMisc + sizeof(Misc) + 1024; }
 
-// Bounded wait; after the first timeout in the CTA every later wait returns at
-// once, so all roles run to the end and TMEM is released.
+// Bounded wait; after the first timeout in the CTA every later wait that is not over
+// already returns at once, so all roles run to the end and TMEM is released.
 __device__ __forceinline__ bool wait_or_abort(Misc& ms, uint64_t* bar, uint32_t parity, int32_t* err) {
+  if (mbar_test(bar, parity)) return true;
   if (*reinterpret_cast<volatile int32_t*>(&ms.abort)) return false;
   if (mbar_wait(bar, parity)) return true;
   *reinterpret_cast<volatile int32_t*>(&ms.abort) = 1;
@@ -165,120 +167,156 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   named_bar(1, kConvert);
 #pragma unroll
   for (int i = 0; i < kConvert / 32; ++i) top = fmaxf(top, ms.red[i]);
-  if (ct == 0) ms.v_max = top;  // read by the softmax after sc_full, or after the CTA's last barrier
-  const float inv_top = 1.0f / top;
+  if (ct == 0) ms.v_max = top;
+  named_bar(2, kConvert + 32);  // for the look-up warp, which passes it on
+  const Unit<D> un(ct);
+  uint4 kx[2][C::kUnits], vx[2][C::kUnits];  // a pair of tiles on its way
+  auto load = [&](int u, const uint8_t* codes, uint4 (&x)[2][C::kUnits]) {
+    if (2 * u < w.count) wait_or_abort(ms, &ms.at_full[u % kPairBufs], (u / kPairBufs) & 1, a.err);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (2 * u + j < w.count) load_units<D>(ms.src[(2 * u + j) % (2 * kPairBufs)], codes, un, x[j]);
+  };
+  auto store = [&](int u, uint32_t off, uint64_t* full, uint64_t* free, const uint4 (&x)[2][C::kUnits]) {
+    const int st = u % kStages;
+    if (u >= kStages) wait_or_abort(ms, &free[st], (u / kStages - 1) & 1, a.err);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int t = 2 * u + j;
+      if (t < w.count)
+        store_units<D>(smem + off + (2 * st + j) * C::kTileBytes, un, x[j], w.n - w.tiles.at(t) * kTile);
+    }
+    fence_proxy_async();
+    mbar_arrive(&full[st]);
+  };
+  load(0, kc, kx);
+  load(0, vc, vx);
+  for (int u = 0; 2 * u < w.count; ++u) {
+    store(u, C::kOffK, ms.k_full, ms.k_free, kx);
+    load(u + 1, kc, kx);
+    store(u, C::kOffV, ms.v_full, ms.v_free, vx);
+    load(u + 1, vc, vx);
+  }
+}
 
-  // where the tile's tokens are, and their scales, 16 tokens a lane of the first warp
-  auto look_up = [&](int t) {
-    if (ct >= 32 || t >= w.count) return;
-    const int sb = t % kScaleBufs;
-    if (ct < kGroups) {
-      const int tok = w.tiles.at(t) * kTile + 16 * ct;
-      float ks = -1.f, vs = 1.f;
-      int64_t src = -1;
+// ------------------------------------------------------------------ addresses and scales
+
+// Four pairs of tiles at a time, 16 tokens a lane: where they are, and their scales.
+template <int D>
+__device__ void look_up_role(const Kv8AttnArgs& a, const Part& w, Misc& ms) {
+  const int lane = threadIdx.x & 31, g = lane % kGroups, P = a.cache.rows_per_block, shift = 31 - __clz(P);
+  float inv_top = 0.f;
+  for (int u0 = 0; 2 * u0 < w.count; u0 += 4) {
+    const int t = 2 * u0 + lane / kGroups, sb = t % (2 * kPairBufs);
+    float ks = -1.f, vs = 1.f;
+    int64_t src = -1;
+    if (t < w.count) {
+      const int tok = w.tiles.at(t) * kTile + 16 * g;
       if (tok < w.n) {
         const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok >> shift);
         if (blk >= 0) {
-          const int64_t at = (int64_t)blk * Hk + w.kvh;
+          const int64_t at = (int64_t)blk * a.cache.kv_heads + w.kvh;
           src = (at * P + (tok & (P - 1))) * D;
           ks = a.cache.k_scale[at];
-          vs = fmaxf(a.cache.v_scale[at] * inv_top, kKv8MinScale);
+          vs = a.cache.v_scale[at];
         } else {
           record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
         }
       }
-      ms.src[sb][ct] = src;
-      ms.ks[sb][ct] = ks;
-      ms.lv[sb][ct] = log2f(vs);
-      ms.rv[sb][ct] = 1.0f / vs;
+    }
+    if (u0 == 0) {
+      named_bar(2, kConvert + 32);
+      inv_top = 1.0f / ms.v_max;
+    } else if (u0 >= kPairBufs) {
+      for (int u = u0; u < u0 + 4 && 2 * u < w.count; ++u)
+        wait_or_abort(ms, &ms.at_free[u % kPairBufs], (u / kPairBufs - 1) & 1, a.err);
+    }
+    if (t < w.count) {
+      if (src >= 0) vs = fmaxf(vs * inv_top, kKv8MinScale);
+      ms.src[sb][g] = src;
+      ms.ks[sb][g] = ks;
+      ms.lv[sb][g] = log2f(vs);
+      ms.rv[sb][g] = 1.0f / vs;
     }
     __syncwarp();
-    if (ct == 0) mbar_arrive(&ms.sc_full[sb]);
-  };
-  const Unit<D> un(ct);
-  uint4 kx[C::kUnits], vx[C::kUnits];
-  look_up(0);
-  look_up(1);
-  named_bar(1, kConvert);
-  if (w.count > 0) {
-    load_units<D>(ms.src[0], kc, un, kx);
-    load_units<D>(ms.src[0], vc, un, vx);
+    if (lane == 0)
+      for (int u = u0; u < u0 + 4 && 2 * u < w.count; ++u) mbar_arrive(&ms.at_full[u % kPairBufs]);
   }
-  for (int t = 0; t < w.count; ++t) {
-    const int st = t & 1, left = w.n - w.tiles.at(t) * kTile;
-    const uint32_t prev = ((t >> 1) & 1) ^ 1;  // the use of the stage before this one
-    if (t >= 2) wait_or_abort(ms, &ms.k_free[st], prev, a.err);
-    store_units<D>(smem + C::kOffK + st * C::kTileBytes, un, kx, left);
-    fence_proxy_async();
-    mbar_arrive(&ms.k_full[st]);
-    // tile t - 3 and all before it are done with (v_free, one tile ago): its place takes tile t + 2
-    look_up(t + 2);
-    const int64_t* src = ms.src[(t + 1) % kScaleBufs];
-    if (t + 1 < w.count) load_units<D>(src, kc, un, kx);
-    if (t >= 2) wait_or_abort(ms, &ms.v_free[st], prev, a.err);
-    store_units<D>(smem + C::kOffV + st * C::kTileBytes, un, vx, left);
-    fence_proxy_async();
-    mbar_arrive(&ms.v_full[st]);
-    if (t + 1 < w.count) load_units<D>(src, vc, un, vx);
-    named_bar(1, kConvert);  // the next tile's addresses
-  }
+  if (w.count == 0) named_bar(2, kConvert + 32);
 }
 
 // ------------------------------------------------------------------ products
 
+// The whole warp runs this, so that descriptors stay in uniform registers; one lane issues.
 template <int D>
-__device__ void mma_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem) {
+__device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem_v) {
   using C = Cfg<D>;
   constexpr uint32_t idesc_s = idesc_f16(kM, kTile, 0, 0);  // Q and K, both K-major
   constexpr uint32_t idesc_o = idesc_f16(kM, D, 0, 1);      // P from TMEM, V [token][dim] MN-major
-  const uint64_t d_q = sdesc_sw128(smem_u32(smem), 16, 1024);
-  const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
-  const uint64_t d_v = sdesc_sw128(smem_u32(smem + C::kOffV), C::kAtom, 1024);
-  const int n = w.count;
+  const uint32_t base = uniform(smem_u32(smem)), tmem = uniform(tmem_v);
+  const uint64_t d_q = sdesc_sw128(base, 16, 1024);
+  const uint64_t d_k = sdesc_sw128(base + C::kOffK, 16, 1024);
+  const uint64_t d_v = sdesc_sw128(base + C::kOffV, C::kAtom, 1024);
+  const int n = uniform(w.count);
+  const bool lead = elect_one();
   bool ok = wait_or_abort(ms, &ms.q_full, 0, a.err);
-  auto product_s = [&](int i, int t) {
-    const uint32_t ko = ((t & 1) * C::kTileBytes) >> 4, qo = (i * C::kTileBytes) >> 4;
-    if (ok) {
+  auto products_s = [&](int t) {  // S_0(t), S_1(t)
+    const int st = (t >> 1) % kStages;
+    if (!(t & 1)) ok = ok && wait_or_abort(ms, &ms.k_full[st], (t >> 1) / kStages & 1, a.err);
+    const uint32_t ko = (t % (2 * kStages) * C::kTileBytes) >> 4;
+    if (lead) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t at = ((ks >> 2) * C::kAtom + (ks & 3) * 32) >> 4;
-        mma_bf16(tmem + C::kColS + kTile * i, d_q + qo + at, d_k + ko + at, idesc_s, ks > 0);
+      for (int i = 0; i < kMTiles; ++i) {
+        if (ok) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_bf16(tmem + kTile * (2 * i + (t & 1)),
+                     d_q + ((i * C::kQBytes + (ks >> 2) * C::kQAtom + (ks & 3) * 32) >> 4),
+                     d_k + ko + (((ks >> 2) * C::kAtom + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+        }
+        mma_commit(&ms.s_full[i][t & 1]);
       }
+      if (t & 1) mma_commit(&ms.k_free[st]);
     }
-    mma_commit(&ms.s_full[i]);
+    __syncwarp();
   };
-  auto product_o = [&](int i, int t) {
-    ok = ok && wait_or_abort(ms, &ms.v_full[t & 1], (t >> 1) & 1, a.err);
-    ok = ok && wait_or_abort(ms, &ms.p_full[i], t & 1, a.err);
-    tc_fence_after();
-    const uint32_t vo = ((t & 1) * C::kTileBytes) >> 4;
-    if (ok) {
-#pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks)
-        mma_f16_ts(tmem + C::kColO + D * i, tmem + C::kColS + kTile * i + 8 * ks, d_v + vo + ((ks * 2048) >> 4), idesc_o,
-                   (t | ks) != 0);
-    }
-    mma_commit(&ms.o_done[i]);
-  };
+  if (n > 0) products_s(0);
   for (int t = 0; t < n; ++t) {
-    ok = ok && wait_or_abort(ms, &ms.k_full[t & 1], (t >> 1) & 1, a.err);
-    tc_fence_after();
-    product_s(0, t);
-    if (t > 0) {
-      product_o(1, t - 1);
-      mma_commit(&ms.v_free[(t - 1) & 1]);
+    if (t + 1 < n) products_s(t + 1);  // over P_i(t - 1), which O_i(t - 1) has read
+    const int st = (t >> 1) % kStages;
+    if (!(t & 1)) ok = ok && wait_or_abort(ms, &ms.v_full[st], (t >> 1) / kStages & 1, a.err);
+    const uint32_t vo = (t % (2 * kStages) * C::kTileBytes) >> 4;
+#pragma unroll
+    for (int i = 0; i < kMTiles; ++i) {
+      ok = ok && wait_or_abort(ms, &ms.p_full[i][t & 1], (t >> 1) & 1, a.err);
+      tc_fence_after();
+      if (lead) {
+        if (ok) {
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_f16_ts(tmem + C::kColO + D * i, tmem + kTile * (2 * i + (t & 1)) + 8 * ks, d_v + vo + ((ks * 2048) >> 4),
+                       idesc_o, (t | ks) != 0);
+        }
+        mma_commit(&ms.o_done[i][t & 1]);
+        if (i == kMTiles - 1 && (t & 1)) mma_commit(&ms.v_free[st]);
+      }
+      __syncwarp();
     }
-    product_s(1, t);
-    mma_commit(&ms.k_free[t & 1]);
-    product_o(0, t);
   }
-  if (n > 0) product_o(1, n - 1);
   // nothing may still write TMEM when it is released, even after a timeout
-  mma_commit(&ms.mma_done);
+  if (lead) mma_commit(&ms.mma_done);
+  __syncwarp();
   mbar_wait(&ms.mma_done, 0);
 }
 
 // ------------------------------------------------------------------ softmax
+
+// Bits [a, b) of 64, whatever a and b are.
+__device__ __forceinline__ uint64_t key_bits(int64_t a, int64_t b) {
+  a = max((int64_t)0, min((int64_t)64, a));
+  b = max(a, min((int64_t)64, b));
+  return (b >= 64 ? ~0ull : (1ull << b) - 1) & ~(a >= 64 ? ~0ull : (1ull << a) - 1);
+}
 
 template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem, int st) {
@@ -291,7 +329,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
   // ---- the row of Q, scaled by a power of two to [1, 2), as f16
   float p2 = 1.f;
   {
-    uint8_t* tile = smem + i * C::kTileBytes;
+    uint8_t* tile = smem + i * C::kQBytes;
     const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + row * a.q_stride + (int64_t)head * D;
     auto piece = [&](int c) {  // 8 dims
       if (!real) return make_uint4(0, 0, 0, 0);
@@ -334,70 +372,59 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
   const int first = real && a.mask.first ? max(0, a.mask.first[row]) : 0;
   const int lo = real && a.mask.window > 0 ? max(first, p - a.mask.window + 1) : first;
   const uint32_t lane_addr = tmem + ((uint32_t)(32 * ((st >> 5) & 3)) << 16);
-  const uint32_t s_addr = lane_addr + C::kColS + kTile * i, o_addr = lane_addr + C::kColO + D * i;
+  const uint32_t o_addr = lane_addr + C::kColO + D * i;
   float m = -FLT_MAX, l = 0.f;
 
   for (int t = 0; t < w.count; ++t) {
-    const int sb = t % kScaleBufs, t0 = w.tiles.at(t) * kTile;
-    wait_or_abort(ms, &ms.sc_full[sb], (t / kScaleBufs) & 1, a.err);
-    bool mapped = true;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) mapped &= ms.ks[sb][g] >= 0.f;
-    const bool whole = t0 >= first && t0 + kTile <= w.n && ((t0 >= lo && t0 + kTile - 1 <= p) || t0 + kTile <= w.pre);
-    const bool plain = __all_sync(0xffffffffu, whole && mapped);
-    wait_or_abort(ms, &ms.s_full[i], t & 1, a.err);
-    tc_fence_after();
-    float x[kHalf];
-    auto load = [&](int h) {
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 16) tmem_ld16(s_addr + kHalf * h + c, x + c);
-      tmem_wait_ld();
-    };
+    const int u = t >> 1, sb = t % (2 * kPairBufs), t0 = w.tiles.at(t) * kTile;
+    const uint32_t s_addr = lane_addr + kTile * (2 * i + (t & 1));
+    wait_or_abort(ms, &ms.at_full[u % kPairBufs], (u / kPairBufs) & 1, a.err);
     // what turns the accumulator's 16 columns into scores in log2 units, before the cap; not 0, so
     // that it leaves -inf alone
-    auto factor = [&](int h, int j) { return fmaxf(fac * ms.ks[sb][h * (kHalf / 16) + j], FLT_MIN); };
-    auto finish = [&](int h) {
-      if constexpr (CAP || BIAS) {
+    float f[kGroups];
+    bool mapped = true;
 #pragma unroll
-        for (int j = 0; j < kHalf / 16; ++j) {
-          const float f = factor(h, j);
+    for (int g = 0; g < kGroups; ++g) {
+      const float ks = ms.ks[sb][g];
+      mapped &= ks >= 0.f;
+      f[g] = fmaxf(fac * ks, FLT_MIN);
+    }
+    const bool whole = t0 >= first && t0 + kTile <= w.n && ((t0 >= lo && t0 + kTile - 1 <= p) || t0 + kTile <= w.pre);
+    const bool plain = __all_sync(0xffffffffu, whole && mapped);
+    wait_or_abort(ms, &ms.s_full[i][t & 1], u & 1, a.err);
+    tc_fence_after();
+    float x[kTile];
 #pragma unroll
-          for (int k = 16 * j; k < 16 * j + 16; ++k) {
-            float y = x[k] * f;
-            if constexpr (CAP) y = post * tanh_exp(y);
-            if constexpr (BIAS) y -= slope * fabsf((float)(p - t0 - kHalf * h) - (float)k);
-            x[k] = y;
-          }
-        }
+    for (int g = 0; g < kGroups; ++g) tmem_ld16(s_addr + 16 * g, x + 16 * g);
+    tmem_wait_ld();
+    if constexpr (CAP || BIAS) {
+#pragma unroll
+      for (int k = 0; k < kTile; ++k) {
+        float y = x[k] * f[k / 16];
+        if constexpr (CAP) y = post * tanh_exp(y);
+        if constexpr (BIAS) y -= slope * fabsf((float)(p - t0) - (float)k);
+        x[k] = y;
       }
-      if (!plain) {
+    }
+    if (!plain) {
+      // a bit for each key that the row sees
+      uint64_t see = key_bits(lo - t0, (int64_t)p + 1 - t0) | key_bits(first - t0, w.pre - t0);
+      see &= key_bits(first - t0, w.n - t0);
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k) {
-          const int key = t0 + kHalf * h + k;
-          const bool see = key < w.n && key >= first && (key < w.pre || (key <= p && key >= lo)) &&
-                           ms.ks[sb][h * (kHalf / 16) + k / 16] >= 0.f;
-          x[k] = see ? x[k] : -INFINITY;
-        }
-      }
-    };
-
-    // ---- the tile's maximum
+      for (int g = 0; g < kGroups; ++g)
+        if (ms.ks[sb][g] < 0.f) see &= ~(0xffffull << (16 * g));
+#pragma unroll
+      for (int k = 0; k < kTile; ++k) x[k] = see >> k & 1 ? x[k] : -INFINITY;
+    }
     float mt = -INFINITY;
-#pragma unroll 1
-    for (int h = 0; h < kTile / kHalf; ++h) {
-      load(h);
-      // the cap rises with the accumulator: without a bias or a mask only the maximum is capped
-      const bool raw = CAP && !BIAS && plain;
-      if (!raw) finish(h);
 #pragma unroll
-      for (int j = 0; j < kHalf / 16; ++j) {
-        float z = x[16 * j];
+    for (int g = 0; g < kGroups; ++g) {
+      const float* y = x + 16 * g;
+      float z[4];
 #pragma unroll
-        for (int k = 1; k < 16; ++k) z = fmaxf(z, x[16 * j + k]);
-        if (raw) z = post * tanh_exp(z * factor(h, j));
-        else if (!CAP && !BIAS) z *= factor(h, j);
-        mt = fmaxf(mt, z);
-      }
+      for (int k = 0; k < 4; ++k) z[k] = fmaxf(fmaxf(y[k], y[k + 4]), fmaxf(y[k + 8], y[k + 12]));
+      const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+      mt = fmaxf(mt, CAP || BIAS ? top : top * f[g]);
     }
     if (__any_sync(0xffffffffu, mt > m + kRescaleMargin)) {
       const float mn = fmaxf(m, mt), alpha = fast_exp2(m - mn);
@@ -405,52 +432,49 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
       l *= alpha;
       if (t > 0) {
         // O holds exactly the tiles before t once O(t-1) is complete
-        wait_or_abort(ms, &ms.o_done[i], (t - 1) & 1, a.err);
+        wait_or_abort(ms, &ms.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1, a.err);
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
           tmem_ld16(o_addr + c, o);
-          tmem_ld16(o_addr + c + 16, o + 16);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= alpha;
+          for (int k = 0; k < 16; ++k) o[k] *= alpha;
           tmem_st16(o_addr + c, o);
-          tmem_st16(o_addr + c + 16, o + 16);
         }
       }
     }
-    // ---- P over S: the first half's 32 columns end before the second half's scores begin
+    // ---- P over S
     const float shift = kPShift - m;
-#pragma unroll 1
-    for (int h = 0; h < kTile / kHalf; ++h) {
-      load(h);
-      finish(h);
 #pragma unroll
-      for (int j = 0; j < kHalf / 16; ++j) {
-        const float f = factor(h, j), add = shift + ms.lv[sb][h * (kHalf / 16) + j];
-        float s0 = 0.f, s1 = 0.f;
-        uint32_t pw[8];
+    for (int g = 0; g < kGroups; ++g) {
+      const float add = shift + ms.lv[sb][g];
+      const float* y = x + 16 * g;
+      float2 sum = make_float2(0.f, 0.f);
+      uint32_t pw[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float x0 = x[16 * j + 2 * k], x1 = x[16 * j + 2 * k + 1];
-          const float y0 = fast_exp2(CAP || BIAS ? x0 + add : fmaf(x0, f, add));
-          const float y1 = fast_exp2(CAP || BIAS ? x1 + add : fmaf(x1, f, add));
-          s0 += y0;
-          s1 += y1;
-          pw[k] = f32x2_to_f16x2(y0, y1);
-        }
-        l = fmaf(s0 + s1, ms.rv[sb][h * (kHalf / 16) + j], l);
-        tmem_st8(s_addr + kHalf / 2 * h + 8 * j, pw);
+      for (int k = 0; k < 8; ++k) {
+        float2 e = make_float2(y[2 * k], y[2 * k + 1]);
+        e = CAP || BIAS ? add2(e, make_float2(add, add)) : fma2(e, make_float2(f[g], f[g]), make_float2(add, add));
+        e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+        sum = k ? add2(sum, e) : e;
+        pw[k] = f32x2_to_f16x2(e.x, e.y);
       }
+      l = fmaf(sum.x + sum.y, ms.rv[sb][g], l);
+      tmem_st8(s_addr + 8 * g, pw);
     }
     tmem_wait_st();
     tc_fence_before();
-    mbar_arrive(&ms.p_full[i]);
+    mbar_arrive(&ms.p_full[i][t & 1]);
+    if (t & 1) {  // the pair's scales are read
+      __syncwarp();
+      if ((st & 31) == 0) mbar_arrive(&ms.at_free[u % kPairBufs]);
+    }
   }
 
   // ---- result
-  if (w.count > 0) wait_or_abort(ms, &ms.o_done[i], (w.count - 1) & 1, a.err);
+  if (w.count > 0) wait_or_abort(ms, &ms.o_done[i][(w.count - 1) & 1], ((w.count - 1) >> 1) & 1, a.err);
   tc_fence_after();
   const float inv = l == 0.f ? 0.f : ms.v_max / l;
   uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (row * a.heads + head) * D;
@@ -483,20 +507,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   Misc& ms = *reinterpret_cast<Misc*>(smem + C::kOffMisc);
-  const int tid = threadIdx.x, wid = tid >> 5;
+  const int tid = threadIdx.x, wid = uniform(tid >> 5);
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&ms.k_full[s], kConvert);
       mbar_init(&ms.v_full[s], kConvert);
       mbar_init(&ms.k_free[s], 1);
       mbar_init(&ms.v_free[s], 1);
     }
     for (int i = 0; i < kMTiles; ++i) {
-      mbar_init(&ms.s_full[i], 1);
-      mbar_init(&ms.p_full[i], 128);
-      mbar_init(&ms.o_done[i], 1);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&ms.s_full[i][s], 1);
+        mbar_init(&ms.p_full[i][s], 128);
+        mbar_init(&ms.o_done[i][s], 1);
+      }
     }
-    for (int i = 0; i < kScaleBufs; ++i) mbar_init(&ms.sc_full[i], 1);
+    for (int u = 0; u < kPairBufs; ++u) {
+      mbar_init(&ms.at_full[u], 1);
+      mbar_init(&ms.at_free[u], kSoftmax / 32);
+    }
     mbar_init(&ms.q_full, kSoftmax);
     mbar_init(&ms.mma_done, 1);
     ms.abort = 0;
@@ -542,12 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
-  if (tid < kSoftmax) {
+  if (wid < kSoftmax / 32) {
     softmax_role<D, CAP, BIAS>(a, w, smem, ms, tmem, tid);
   } else {
-    if (tid < kSoftmax + kConvert) convert_role<D>(a, w, smem, ms, tid - kSoftmax);
-    else if (tid == kSoftmax + kConvert) mma_role<D>(a, w, smem, ms, tmem);
-    __syncwarp();
+    if (wid < kMmaWarp) convert_role<D>(a, w, smem, ms, tid - kSoftmax);
+    else if (wid == kLookWarp) look_up_role<D>(a, w, ms);
+    else mma_role<D>(a, w, smem, ms, tmem);
   }
   __syncthreads();
   tc_fence_after();
