@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
       }
     }
     const bool cap = a.mask.softcap > 0.f, bias = a.mask.slopes != nullptr;
-    const float pre_mul = cap ? 1.0f / a.mask.softcap : kLog2e, post_mul = a.mask.softcap * kLog2e;
+    const float pre_mul = cap ? 2.0f * kLog2e / a.mask.softcap : kLog2e, post_mul = a.mask.softcap * kLog2e;
 
     float o[NB][C::kMb][4], m[NB][2], l[NB][2], vref = kKv8MinScale;
 #pragma unroll
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[nb][i] = post_mul * tanh_exp(sc[nb][i]);
+          for (int i = 0; i < 4; ++i) sc[nb][i] = post_mul * tanh_exp2(sc[nb][i]);
       }
       if (bias) {
 #pragma unroll

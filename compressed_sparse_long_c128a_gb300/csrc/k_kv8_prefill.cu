@@ -364,7 +364,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     mbar_arrive(&ms.q_full);
   }
 
-  const float fac = p2 * a.mask.scale * (CAP ? 1.0f / a.mask.softcap : kLog2e);
+  const float fac = p2 * a.mask.scale * (CAP ? 2.0f * kLog2e / a.mask.softcap : kLog2e);
   const float post = a.mask.softcap * kLog2e;
   const float slope = BIAS && real ? a.mask.slopes[head] * kLog2e : 0.f;
   // rows that do not exist see every key, so that they ask for no mask
@@ -397,18 +397,17 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) tmem_ld16(s_addr + 16 * g, x + 16 * g);
     tmem_wait_ld();
-    if constexpr (CAP || BIAS) {
+    if constexpr (BIAS) {
 #pragma unroll
       for (int k = 0; k < kTile; ++k) {
         float y = x[k] * f[k / 16];
-        if constexpr (CAP) y = post * tanh_exp(y);
-        if constexpr (BIAS) y -= slope * fabsf((float)(p - t0) - (float)k);
-        x[k] = y;
+        if constexpr (CAP) y = post * tanh_exp2(y);
+        x[k] = y - slope * fabsf((float)(p - t0) - (float)k);
       }
     }
+    uint64_t see = ~0ull;  // a bit for each key that the row sees
     if (!plain) {
-      // a bit for each key that the row sees
-      uint64_t see = key_bits(lo - t0, (int64_t)p + 1 - t0) | key_bits(first - t0, w.pre - t0);
+      see = key_bits(lo - t0, (int64_t)p + 1 - t0) | key_bits(first - t0, w.pre - t0);
       see &= key_bits(first - t0, w.n - t0);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g)
@@ -416,6 +415,8 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
       for (int k = 0; k < kTile; ++k) x[k] = see >> k & 1 ? x[k] : -INFINITY;
     }
+    // the cap rises with the accumulator: without a bias only the maximum is capped here (one over
+    // hidden keys alone gives -cap, at or below every score)
     float mt = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
@@ -424,7 +425,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[k] = fmaxf(fmaxf(y[k], y[k + 4]), fmaxf(y[k + 8], y[k + 12]));
       const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-      mt = fmaxf(mt, CAP || BIAS ? top : top * f[g]);
+      mt = fmaxf(mt, BIAS ? top : CAP ? post * tanh_exp2(top * f[g]) : top * f[g]);
     }
     if (__any_sync(0xffffffffu, mt > m + kRescaleMargin)) {
       const float mn = fmaxf(m, mt), alpha = fast_exp2(m - mn);
@@ -456,8 +457,23 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         float2 e = make_float2(y[2 * k], y[2 * k + 1]);
-        e = CAP || BIAS ? add2(e, make_float2(add, add)) : fma2(e, make_float2(f[g], f[g]), make_float2(add, add));
+        if constexpr (BIAS) {
+          e = add2(e, make_float2(add, add));
+        } else if constexpr (CAP) {  // post tanh + add
+          e = make_float2(fast_exp2(e.x * f[g]), fast_exp2(e.y * f[g]));
+          e = add2(e, make_float2(1.f, 1.f));
+          e = make_float2(fast_rcp(e.x), fast_rcp(e.y));
+          e = fma2(e, make_float2(-2.f * post, -2.f * post), make_float2(post + add, post + add));
+        } else {
+          e = fma2(e, make_float2(f[g], f[g]), make_float2(add, add));
+        }
         e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+        if constexpr (CAP && !BIAS) {  // -inf does not pass the cap
+          if (!plain) {
+            e.x = see >> (16 * g + 2 * k) & 1 ? e.x : 0.f;
+            e.y = see >> (16 * g + 2 * k + 1) & 1 ? e.y : 0.f;
+          }
+        }
         sum = k ? add2(sum, e) : e;
         pw[k] = f32x2_to_f16x2(e.x, e.y);
       }

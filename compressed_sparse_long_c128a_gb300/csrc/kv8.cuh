@@ -108,10 +108,13 @@ __device__ __forceinline__ float pow2_floor(float x) {
 }
 __device__ __forceinline__ float pow2_recip(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
-// tanh(x) = sign(x) (1 - 2 / (e^(2|x|) + 1)): about 2e-7 off, absolutely.
-__device__ __forceinline__ float tanh_exp(float x) {
-  const float e = fast_exp2(fabsf(x) * 2.885390081777927f);  // 2 log2(e)
-  return copysignf(1.0f - __fdividef(2.0f, e + 1.0f), x);
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+
+// tanh(x) = 1 - 2 / (e^(2 x) + 1), of x 2 log2(e): about 2e-7 off, absolutely, for any x.
+__device__ __forceinline__ float tanh_exp2(float x) { return fmaf(-2.0f, fast_rcp(fast_exp2(x) + 1.0f), 1.0f); }
 
 }  // namespace csa
