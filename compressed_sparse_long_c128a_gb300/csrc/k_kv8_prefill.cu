@@ -126,7 +126,7 @@ __device__ __forceinline__ void load_units(const int64_t* src, const uint8_t* co
 }
 
 // `left`: rows of the tile that hold tokens; the others become zeros
-template <int D>
+template <int D, bool WHOLE>
 __device__ __forceinline__ void store_units(uint8_t* tile, const Unit<D>& un, const uint4* x, int left) {
   constexpr int kRows = kConvert / (D / 16);
   uint8_t* at0 = tile + sw128_offset(un.row, 16 * un.piece, kTile);
@@ -134,7 +134,7 @@ __device__ __forceinline__ void store_units(uint8_t* tile, const Unit<D>& un, co
 #pragma unroll
   for (int i = 0; i < Cfg<D>::kUnits; ++i) {  // rows a multiple of 8 apart: the swizzle stays
     uint4 lo, hi;
-    const bool there = un.row + i * kRows < left;
+    const bool there = WHOLE || un.row + i * kRows < left;
     e4m3x4_to_f16x2(there ? x[i].x : 0u, lo.x, lo.y);
     e4m3x4_to_f16x2(there ? x[i].y : 0u, lo.z, lo.w);
     e4m3x4_to_f16x2(there ? x[i].z : 0u, hi.x, hi.y);
@@ -183,8 +183,11 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = 2 * u + j;
-      if (t < w.count)
-        store_units<D>(smem + off + (2 * st + j) * C::kTileBytes, un, x[j], w.n - w.tiles.at(t) * kTile);
+      if (t >= w.count) break;
+      const int left = w.n - w.tiles.at(t) * kTile;
+      uint8_t* tile = smem + off + (2 * st + j) * C::kTileBytes;
+      if (left >= kTile) store_units<D, true>(tile, un, x[j], left);
+      else store_units<D, false>(tile, un, x[j], left);
     }
     fence_proxy_async();
     mbar_arrive(&full[st]);
