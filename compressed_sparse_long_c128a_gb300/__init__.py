@@ -319,6 +319,10 @@ def sparse_attn_prefill(layer: Layer, q, seq_id, pos, comp: PagedCache, comp_bt,
 # ------------------------------------------------------------------ step plan, 8-bit key / value cache
 
 
+# These calls are short next to their launches, so the checks ask each tensor for little:
+# raw device and stream numbers, one look at its shape and strides.
+
+
 def _dev(t, dtype, what, device):
     """Device pointer of a dense tensor of the given type on `device`."""
     if t.dtype is not dtype or not t.is_contiguous():
@@ -328,13 +332,26 @@ def _dev(t, dtype, what, device):
     return t.data_ptr()
 
 
-def _rows3(t, what, device):
-    """(pointer, elements between rows) of [rows, heads, dim] rows whose heads are dense."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] != 1):
+def _rows3(t, what, shape, device):
+    """(pointer, elements between rows, type) of [rows, heads, dim] rows whose heads are dense."""
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1 or (st[1] != shape[2] and shape[1] != 1):
         raise ValueError(f"{what} must be [rows, heads, dim] with dense heads")
     if t.get_device() != device:
         raise ValueError(f"{what} must live on the current CUDA device")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), st[0], _tdtype(t)
+
+
+def _current(t):
+    """The current device; t, the call's first tensor, must live there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the tensors must live on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 @dataclass
@@ -360,6 +377,7 @@ class Kv8Cache:
             if t.device != self.k.device:
                 raise ValueError("the cache's tensors must live on one device")
         self.num_blocks, self.kv_heads, self.rows_per_block, self.dim = shape
+        self.device = self.k.get_device()
         self._c = Kv8C(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), shape[0], shape[2],
                        shape[1], shape[3])
 
@@ -378,47 +396,51 @@ def step_plan(cached, n_new, free_blocks, bt, block_positions: int, num_blocks: 
               used, err, stream=None):
     """Row starts, sequence ids, positions, slots and the block table of a step from its requests' lengths
     (slot may be None).  bt [num_reqs, stride] is updated in place; rows past the step's become padding (-1)."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
-    if bt.dim() != 2 or cached.numel() != bt.shape[0] or n_new.numel() != bt.shape[0]:
+    dev, i32 = _current(bt), torch.int32
+    shape, n_rows = bt.shape, seq_id.numel()
+    if len(shape) != 2 or cached.numel() != shape[0] or n_new.numel() != shape[0]:
         raise ValueError("cached and n_new must have one entry for each row of the block table")
-    if row_start.numel() != bt.shape[0] + 1 or pos.numel() != seq_id.numel() or used.numel() != 1:
+    if row_start.numel() != shape[0] + 1 or pos.numel() != n_rows or used.numel() != 1:
         raise ValueError("row_start must be [num_reqs + 1], seq_id and pos of one length, used [1]")
-    if slot is not None and slot.numel() != seq_id.numel():
+    if slot is not None and slot.numel() != n_rows:
         raise ValueError("slot must have the length of seq_id")
-    st = lib().csa_step_plan(_dev(cached, i32, "cached", dev), _dev(n_new, i32, "n_new", dev), bt.shape[0],
+    st = lib().csa_step_plan(_dev(cached, i32, "cached", dev), _dev(n_new, i32, "n_new", dev), shape[0],
                              _dev(free_blocks, i32, "free_blocks", dev), free_blocks.numel(),
-                             _dev(bt, i32, "block table", dev), bt.shape[1], block_positions, num_blocks,
-                             seq_id.numel(), _dev(row_start, i32, "row_start", dev), _dev(seq_id, i32, "seq_id", dev),
+                             _dev(bt, i32, "block table", dev), shape[1], block_positions, num_blocks, n_rows,
+                             _dev(row_start, i32, "row_start", dev), _dev(seq_id, i32, "seq_id", dev),
                              _dev(pos, i32, "pos", dev),
                              None if slot is None else _dev(slot, torch.int64, "slot", dev),
-                             _dev(used, i32, "used", dev), _dev(err, i32, "err", dev), _stream(stream))
+                             _dev(used, i32, "used", dev), _dev(err, i32, "err", dev), _raw_stream(stream, dev))
     _check(st, "csa_step_plan")
 
 
 def _kv8_lengths(row_start, cached, cache, bt, dev):
     """Pointers of row_start and cached, and the C block table, checked against each other."""
-    if cache.k.get_device() != dev:
+    if cache.device != dev:
         raise ValueError("the cache must live on the current CUDA device")
-    if bt.dim() != 2 or row_start.numel() != bt.shape[0] + 1 or cached.numel() != bt.shape[0]:
+    shape = bt.shape
+    if len(shape) != 2 or row_start.numel() != shape[0] + 1 or cached.numel() != shape[0]:
         raise ValueError("row_start must be [num_seqs + 1] and cached [num_seqs] for the block table's num_seqs")
     i32 = torch.int32
     return (_dev(row_start, i32, "row_start", dev), _dev(cached, i32, "cached", dev),
-            BlockTableC(_dev(bt, i32, "block table", dev), bt.shape[0], bt.shape[1]))
+            BlockTableC(_dev(bt, i32, "block table", dev), shape[0], shape[1]))
 
 
 def kv8_store(k, v, row_start, cached, cache: Kv8Cache, bt, err, stream=None):
     """Insert k, v [n_rows, kv_heads, dim] (f32 or bf16; rows may be strided) into the 8-bit cache: request b's
     rows row_start[b]..row_start[b+1] go to positions cached[b].. of row b of the block table."""
-    dev = torch.cuda.current_device()
-    if k.shape != v.shape or k.dtype is not v.dtype:
+    dev, shape = _current(k), k.shape
+    if shape != v.shape:
         raise ValueError("k and v must have one shape and type")
-    kp, ks = _rows3(k, "k", dev)
-    vp, vs = _rows3(v, "v", dev)
-    if k.shape[1] != cache.kv_heads or k.shape[2] != cache.dim:
+    kp, ks, dt = _rows3(k, "k", shape, dev)
+    vp, vs, vt = _rows3(v, "v", shape, dev)
+    if dt != vt:
+        raise ValueError("k and v must have one shape and type")
+    if shape[1] != cache.kv_heads or shape[2] != cache.dim:
         raise ValueError("k and v must have the cache's heads and dim")
     rs, ca, b = _kv8_lengths(row_start, cached, cache, bt, dev)
-    st = lib().csa_kv8_store(kp, vp, _tdtype(k), ks, vs, k.shape[0], rs, ca, cache.c(), b,
-                             _dev(err, torch.int32, "err", dev), _stream(stream))
+    st = lib().csa_kv8_store(kp, vp, dt, ks, vs, shape[0], rs, ca, cache.c(), b, _dev(err, torch.int32, "err", dev),
+                             _raw_stream(stream, dev))
     _check(st, "csa_kv8_store")
 
 
@@ -433,31 +455,37 @@ def kv8_attn(q, row_start, cached, cache: Kv8Cache, bt, max_new: int, out, ws, e
     softcap * tanh(a / softcap), lowered by slopes[head] * distance, and masked by causality, `window`, `first`
     (int32 [n_rows], each row's first visible position) and `prefix` (int32 [num_seqs], tokens every row sees).
     The cache already holds the rows' own tokens; max_new is the most rows of a request."""
-    dev = torch.cuda.current_device()
-    qp, qs = _rows3(q, "q", dev)
-    n_rows, heads, dim = q.shape
-    if dim != cache.dim or out.shape != q.shape:
+    dev, shape = _current(q), q.shape
+    qp, qs, dt = _rows3(q, "q", shape, dev)
+    n_rows, heads, dim = shape
+    if dim != cache.dim or out.shape != shape:
         raise ValueError("q and out must be [n_rows, heads, dim] with the cache's dim")
     rs, ca, b = _kv8_lengths(row_start, cached, cache, bt, dev)
     i32, f32 = torch.int32, torch.float32
-    if slopes is not None and slopes.numel() != heads:
-        raise ValueError("slopes must be [heads]")
-    if first is not None and first.numel() != n_rows:
-        raise ValueError("first must be [n_rows]")
-    if prefix is not None and prefix.numel() != bt.shape[0]:
-        raise ValueError("prefix must be [num_seqs]")
-    if lse is not None and lse.numel() != n_rows * heads:
-        raise ValueError("lse must be [n_rows, heads]")
-    m = Kv8MaskC(dim ** -0.5 if scale is None else scale, softcap, window,
-                 None if slopes is None else _dev(slopes, f32, "slopes", dev),
-                 None if first is None else _dev(first, i32, "first", dev),
-                 None if prefix is None else _dev(prefix, i32, "prefix", dev))
-    st = lib().csa_kv8_attn(qp, _tdtype(q), qs, n_rows, heads, rs, ca, max_new, cache.c(), b, m,
-                            _dev(out, out.dtype, "out", dev), _tdtype(out),
-                            None if lse is None else _dev(lse, f32, "lse", dev),
-                            None if ws is None else _dev(ws, ws.dtype, "ws", dev),
-                            0 if ws is None else ws.numel() * ws.element_size(), _dev(err, i32, "err", dev),
-                            _stream(stream))
+    m = Kv8MaskC(dim ** -0.5 if scale is None else scale, softcap, window)
+    if slopes is not None:
+        if slopes.numel() != heads:
+            raise ValueError("slopes must be [heads]")
+        m.slopes = _dev(slopes, f32, "slopes", dev)
+    if first is not None:
+        if first.numel() != n_rows:
+            raise ValueError("first must be [n_rows]")
+        m.first = _dev(first, i32, "first", dev)
+    if prefix is not None:
+        if prefix.numel() != b.num_seqs:
+            raise ValueError("prefix must be [num_seqs]")
+        m.prefix = _dev(prefix, i32, "prefix", dev)
+    lp = wp = None
+    nbytes = 0
+    if lse is not None:
+        if lse.numel() != n_rows * heads:
+            raise ValueError("lse must be [n_rows, heads]")
+        lp = _dev(lse, f32, "lse", dev)
+    if ws is not None:
+        wp, nbytes = _dev(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size()
+    st = lib().csa_kv8_attn(qp, dt, qs, n_rows, heads, rs, ca, max_new, cache.c(), b, m,
+                            _dev(out, out.dtype, "out", dev), _tdtype(out), lp, wp, nbytes,
+                            _dev(err, i32, "err", dev), _raw_stream(stream, dev))
     _check(st, "csa_kv8_attn")
 
 
