@@ -59,8 +59,11 @@ struct Cfg {
 
 template <int D, int NB>
 constexpr int ctas_per_sm() {
-  return NB == 4 || (D == 256 && NB == 2) ? 2 : Cfg<D>::kCtasPerSm;
+  return D == 64 && NB == 4 ? 3 : NB == 4 || (D == 256 && NB == 2) ? 2 : Cfg<D>::kCtasPerSm;
 }
+
+constexpr int kSms = 152;  // of a GB300; another count only changes how even the shares are
+constexpr int kMaxParts = 4 * kSms;  // CTAs of a deal
 
 // Byte offset of piece c of token r in a stage's key (or value) half; see the header
 // comment for who reads what together.
@@ -187,9 +190,55 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
     const int n_rows = job.r.rows(), n = job.r.len();
     const int chunks = job.pairs / Hk, kvh = pair / chunks, col0 = (pair % chunks) * CC;
     const int n_cols = min(CC, n_rows * G - col0);
+    // column blocks that hold something; the others are left out of the products (a request of one
+    // row beside others of three)
+    const int nbs = NB == 1 ? 1 : (n_cols + 7) / 8;
+
+    // ---- stream: step s of this warp is 16 tokens of tile ti0 + s
+    auto token0 = [&](int s) { return job.tiles.at(ti0 + s) * kTile + wid * kStep; };
+    auto block_of = [&](int s) {
+      if (s >= steps) return -1;
+      const int t0 = token0(s);
+      return t0 < n ? kv8_block(a.bt, a.cache.num_blocks, b, t0 / P) : -1;
+    };
+    auto issue = [&](int s, int blk) {
+      if (s < steps) {
+        const int st = s % ST, t0 = token0(s);
+        const int left = blk >= 0 ? n - t0 : 0;  // tokens there are
+        const int64_t at = (int64_t)max(blk, 0) * Hk + kvh;
+        const int64_t off = (at * P + (t0 & (P - 1))) * D;
+        const uint8_t* ks = reinterpret_cast<const uint8_t*>(a.cache.k) + off;
+        const uint8_t* vs = reinterpret_cast<const uint8_t*>(a.cache.v) + off;
+        const uint32_t dst = my_ring + st * C::kStageBytes;
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          const int x = lane + 32 * i, r = x / CH, c = x % CH;
+          const bool there = r < left;  // else zeros are written and nothing is read
+          tc::cp_async16(dst + piece_offset<D, false>(r, c),
+                         there ? ks + x * 16 : reinterpret_cast<const uint8_t*>(a.cache.k), there ? 16u : 0u);
+          tc::cp_async16(dst + kStep * D + piece_offset<D, true>(r, c),
+                         there ? vs + x * 16 : reinterpret_cast<const uint8_t*>(a.cache.v), there ? 16u : 0u);
+        }
+        if (lane < 2) {
+          if (blk >= 0) {
+            cp_async4(my_scale + (st * 2 + lane) * 4, (lane ? a.cache.v_scale : a.cache.k_scale) + at);
+          } else {
+            s_scale[wid][st][lane] = -1.0f;
+            if (t0 < n) record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
+          }
+        }
+      }
+      tc::cp_async_commit();
+    };
+    int32_t ids[ST];  // the first steps' blocks: looked up together, copied before all else
+#pragma unroll
+    for (int x = 0; x < ST; ++x) ids[x] = block_of(x);
+    __syncthreads();  // the last pair's shared values are read
+#pragma unroll
+    for (int x = 0; x < ST - 1; ++x) issue(x, ids[x]);
+    int32_t next_blk = ids[ST - 1];
 
     // ---- columns: bounds for the masks, and what they leave to all columns alike
-    __syncthreads();  // the last pair's shared values are read
     if (tid < CC) {
       const int i = min((col0 + tid) / G, n_rows - 1), p = job.r.cached + i;
       const int f = a.mask.first ? max(0, a.mask.first[job.r.r0 + i]) : 0;
@@ -265,44 +314,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
       l[nb][0] = l[nb][1] = 0.f;
     }
 
-    // ---- stream: step s of this warp is 16 tokens of tile ti0 + s
-    auto token0 = [&](int s) { return job.tiles.at(ti0 + s) * kTile + wid * kStep; };
-    auto block_of = [&](int s) {
-      if (s >= steps) return -1;
-      const int t0 = token0(s);
-      return t0 < n ? kv8_block(a.bt, a.cache.num_blocks, b, t0 / P) : -1;
-    };
-    auto issue = [&](int s, int blk) {
-      if (s < steps) {
-        const int st = s % ST, t0 = token0(s);
-        const int left = blk >= 0 ? n - t0 : 0;  // tokens there are
-        const int64_t at = (int64_t)max(blk, 0) * Hk + kvh;
-        const int64_t off = (at * P + (t0 & (P - 1))) * D;
-        const uint8_t* ks = reinterpret_cast<const uint8_t*>(a.cache.k) + off;
-        const uint8_t* vs = reinterpret_cast<const uint8_t*>(a.cache.v) + off;
-        const uint32_t dst = my_ring + st * C::kStageBytes;
-#pragma unroll
-        for (int i = 0; i < CH / 2; ++i) {
-          const int x = lane + 32 * i, r = x / CH, c = x % CH;
-          const bool there = r < left;  // else zeros are written and nothing is read
-          tc::cp_async16(dst + piece_offset<D, false>(r, c),
-                         there ? ks + x * 16 : reinterpret_cast<const uint8_t*>(a.cache.k), there ? 16u : 0u);
-          tc::cp_async16(dst + kStep * D + piece_offset<D, true>(r, c),
-                         there ? vs + x * 16 : reinterpret_cast<const uint8_t*>(a.cache.v), there ? 16u : 0u);
-        }
-        if (lane < 2) {
-          if (blk >= 0) {
-            cp_async4(my_scale + (st * 2 + lane) * 4, (lane ? a.cache.v_scale : a.cache.k_scale) + at);
-          } else {
-            s_scale[wid][st][lane] = -1.0f;
-            if (t0 < n) record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
-          }
-        }
-      }
-      tc::cp_async_commit();
-    };
-    for (int s = 0; s < ST - 1; ++s) issue(s, block_of(s));
-    int next_blk = block_of(ST - 1);
     for (int s = 0; s < steps; ++s) {
       tc::cp_async_wait<ST - 2>();
       __syncwarp();
@@ -331,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
           e4m3x4_to_f16x2(xw[i], a0, a2);
           e4m3x4_to_f16x2(yw[i], a1, a3);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16(sc[nb], a0, a1, a2, a3, qf[nb][4 * j + i][0], qf[nb][4 * j + i][1]);
+          for (int nb = 0; nb < NB; ++nb)
+            if (nb == 0 || nb < nbs) mma_f16(sc[nb], a0, a1, a2, a3, qf[nb][4 * j + i][0], qf[nb][4 * j + i][1]);
         }
       }
 
@@ -343,28 +355,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
         for (int i = 0; i < 4; ++i) sc[nb][i] *= fac[nb][i & 1] * mul;
       if (cap) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
+          if (nb >= nbs) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[nb][i] = post_mul * tanh_exp2(sc[nb][i]);
+        }
       }
       if (bias) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
+          if (nb >= nbs) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             sc[nb][i] -= slope[nb][i & 1] * fabsf((float)(c_p[nb * 8 + 2 * t4 + (i & 1)] - (t0 + r0 + 4 * (i & 2))));
+        }
       }
       const bool whole = t0 >= all_first && t0 + kStep <= n &&
                          ((t0 >= all_lo && t0 + kStep - 1 <= all_p) || t0 + kStep <= job.pre);
       if (!whole) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
+          if (nb >= nbs) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = nb * 8 + 2 * t4 + (i & 1), t = t0 + r0 + 4 * (i & 2);
             const bool see = t < n && t >= c_first[c] && (t < job.pre || (t <= c_p[c] && t >= c_lo[c]));
             if (!see) sc[nb][i] = -INFINITY;
           }
+        }
       }
       bool raise = false;
 #pragma unroll
@@ -401,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
       uint32_t pf[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
+        if (nb >= nbs) break;
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -425,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
             e4m3x4_to_f16x2(__byte_perm(x[0], x[1], hf ? 0x7362 : 0x5140), a0, a1);
             e4m3x4_to_f16x2(__byte_perm(x[2], x[3], hf ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][2 * i + hf], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
+            for (int nb = 0; nb < NB; ++nb)
+              if (nb == 0 || nb < nbs) mma_f16(o[nb][2 * i + hf], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
           }
         }
       } else {
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
               e4m3x4_to_f16x2(__byte_perm(word(w[2]), word(w[3]), hf ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
-                mma_f16(o[nb][8 * j + 2 * i + hf], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
+                if (nb == 0 || nb < nbs) mma_f16(o[nb][8 * j + 2 * i + hf], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
             }
           }
         }
@@ -469,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
     const int par = wid & 1, half = wid >> 1;  // this warp's part of the sum: column parity, half of the dims
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
+      if (nb >= nbs) break;
       float mm[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -539,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
 // Joins the parts of the pair that starts in CTA blockIdx.x of the deal and ends in a later one:
 // part 0 in that CTA's second slot, the others in the next CTAs' first slots.
 template <int D, int NB>
-__global__ void __launch_bounds__(128) kv8_decode_join_kernel(const Kv8AttnArgs a) {
+__global__ void __launch_bounds__(kThreads) kv8_decode_join_kernel(const Kv8AttnArgs a) {
   constexpr int CC = 8 * NB;
   pdl_trigger();
   pdl_wait();
@@ -550,23 +571,45 @@ __global__ void __launch_bounds__(128) kv8_decode_join_kernel(const Kv8AttnArgs 
   const int kvh = head[2], cg = head[3] + c, G = a.group;
   const int64_t rh = (int64_t)(head[1] + cg / G) * a.heads + kvh * G + cg % G;
   auto slot = [&](int i) { return (2 * (int64_t)(cta + i) + (i == 0)) * CC + c; };
+  __shared__ float weight[kMaxParts];
+  __shared__ float sums[kWarps][D];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   float m = -FLT_MAX;
-  for (int i = threadIdx.x & 31; i < parts; i += 32) m = fmaxf(m, a.part_ml[2 * slot(i)]);
+  for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[2 * slot(i)]);
   m = warp_max(m);
   float l = 0.f;
-  for (int i = threadIdx.x & 31; i < parts; i += 32) l += a.part_ml[2 * slot(i) + 1] * fast_exp2(a.part_ml[2 * slot(i)] - m);
-  l = warp_sum(l);
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float o = 0.f;
-    for (int i = 0; i < parts; ++i) o += a.part_o[slot(i) * D + d] * fast_exp2(a.part_ml[2 * slot(i)] - m);
-    o *= inv;
-    reinterpret_cast<uint16_t*>(a.out)[rh * D + d] = f32_to_bf16(o);
+  for (int i = lane; i < parts; i += 32) {
+    const float w = fast_exp2(a.part_ml[2 * slot(i)] - m);
+    l += a.part_ml[2 * slot(i) + 1] * w;
+    if (wid == 0) weight[i] = w;
   }
-  if (a.lse && threadIdx.x == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
+  l = warp_sum(l);
+  __syncthreads();
+  // a warp every fourth part, a lane D / 32 dims
+  float o[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
+#pragma unroll 4
+  for (int i = wid; i < parts; i += kWarps) {
+    const float* src = a.part_o + slot(i) * D + lane * (D / 32);
+    const float w = weight[i];
+#pragma unroll
+    for (int k = 0; k < D / 32; k += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + k);
+      o[k] += v.x * w;
+      o[k + 1] += v.y * w;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) sums[wid][lane * (D / 32) + k] = o[k];
+  __syncthreads();
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  for (int d = tid; d < D; d += kThreads)
+    reinterpret_cast<uint16_t*>(a.out)[rh * D + d] =
+        f32_to_bf16(((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) * inv);
+  if (a.lse && tid == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
 }
 
-constexpr int kSms = 152;  // of a GB300; another count only changes how even the shares are
 
 template <int D, int NB>
 cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t s) {
@@ -582,7 +625,7 @@ cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t s) {
   const int32_t n = kSms * ctas_per_sm<D, NB>();
   const cudaError_t k = launch_k(kv8_decode_kernel<D, NB>, dim3(n), dim3(kThreads), Cfg<D>::kSmem, s, 0, a);
   if (k != cudaSuccess) return k;
-  return launch_k(kv8_decode_join_kernel<D, NB>, dim3(n, 8 * NB), dim3(128), 0, s, 0, a);
+  return launch_k(kv8_decode_join_kernel<D, NB>, dim3(n, 8 * NB), dim3(kThreads), 0, s, 0, a);
 }
 
 template <typename F>
