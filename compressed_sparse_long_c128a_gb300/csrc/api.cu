@@ -421,8 +421,10 @@ int csa_step_plan(const int32_t* cached, const int32_t* n_new, int32_t num_reqs,
   if (!row_start || !used || !err || (num_reqs > 0 && (!cached || !n_new || !table)) || (n_free > 0 && !free_blocks) ||
       (n_rows > 0 && (!seq_id || !pos)))
     return CSA_ERR_INVALID_ARG;
+  const uintptr_t al =
+      reinterpret_cast<uintptr_t>(seq_id) | reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(slot);
   PlanArgs a{cached, n_new, num_reqs, free_blocks, n_free, table, stride, block_positions, num_blocks, n_rows,
-             row_start, seq_id, pos, slot, used, err};
+             row_start, seq_id, pos, slot, al % 16 == 0, used, err};
   return cuda_status(launch_plan(a, stream));
 }
 
@@ -436,7 +438,7 @@ int csa_kv8_store(const void* k, const void* v, int32_t in_dtype, int64_t k_stri
   int st = check_kv8(cache);
   if (st) return st;
   if ((st = check_bt(bt))) return st;
-  if ((int64_t)n_rows / cache->rows_per_block + bt->num_seqs > INT32_MAX) return CSA_ERR_UNSUPPORTED;
+  if (((int64_t)n_rows / cache->rows_per_block + bt->num_seqs) * 2 * cache->kv_heads > INT32_MAX) return CSA_ERR_UNSUPPORTED;
   const size_t el = in_dtype == CSA_F32 ? 4 : 2;
   const uintptr_t al = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
   if (al % el) return CSA_ERR_INVALID_ARG;

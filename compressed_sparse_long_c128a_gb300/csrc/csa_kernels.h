@@ -279,6 +279,7 @@ struct PlanArgs {
   int32_t* seq_id;
   int32_t* pos;
   int64_t* slot;  // nullptr: not wanted
+  int32_t vec;    // seq_id, pos and slot may be written 16 bytes at a time
   int32_t* used;
   int32_t* err;
 };

@@ -75,39 +75,59 @@ __global__ void __launch_bounds__(kThreads) kv8_attn_simt_kernel(const Kv8AttnAr
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads wid and wid + 4, the same in every lane
   const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.cache.k);
   const uint8_t* vc = reinterpret_cast<const uint8_t*>(a.cache.v);
-  const int units = D / 16;
+  const int units = D / 16, shift = 31 - __clz(P);
 
-  for (int ti = t0; ti < t1; ++ti) {
-    const int base = (ti < nA ? tA + ti : tB + ti - nA) * kTile;
-    __syncthreads();
-    // codes to fp32, keys and values; a key that no row sees becomes zeros
-    for (int u = tid; u < 2 * kTile * units; u += kThreads) {
+  // a tile's codes and scales wait in registers while the tile before it is worked on
+  constexpr int kMaxUnits = 2 * kTile * (kMaxDim / 16) / kThreads;
+  uint4 code[kMaxUnits];
+  float scl[kMaxUnits];
+  auto tile_base = [&](int ti) { return (ti < nA ? tA + ti : tB + ti - nA) * kTile; };
+  auto fetch = [&](int ti) {
+    const int base = tile_base(ti);
+#pragma unroll
+    for (int i = 0; i < kMaxUnits; ++i) {
+      const int u = tid + i * kThreads;
+      if (u >= 2 * kTile * units) break;
       const bool val = u >= kTile * units;
-      const int w = val ? u - kTile * units : u, j = w / units, d0 = (w - j * units) * 16;
-      const int t = base + j;
-      uint4 c = make_uint4(0, 0, 0, 0);
-      float sc = 0.f;
+      const int w = val ? u - kTile * units : u, j = (unsigned)w / (unsigned)units, t = base + j;
+      code[i] = make_uint4(0, 0, 0, 0);
+      scl[i] = 0.f;
       if (t < n) {
-        const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, b, t / P);
+        const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, b, t >> shift);
         if (blk >= 0) {
           const int64_t at = (int64_t)blk * Hk + kvh;
-          c = __ldg(reinterpret_cast<const uint4*>((val ? vc : kc) + (at * P + t % P) * D + d0));
-          sc = (val ? a.cache.v_scale : a.cache.k_scale)[at];
+          code[i] = __ldg(reinterpret_cast<const uint4*>((val ? vc : kc) + (at * P + (t & (P - 1))) * D) + (w - j * units));
+          scl[i] = (val ? a.cache.v_scale : a.cache.k_scale)[at];
         }
       }
-      const uint32_t k[4] = {c.x, c.y, c.z, c.w};
-      float* dst = (val ? sV : sK) + j * LD + d0;
+    }
+  };
+  if (t0 < t1) fetch(t0);
+  for (int ti = t0; ti < t1; ++ti) {
+    const int base = tile_base(ti);
+    __syncthreads();
+    // codes to fp32, keys and values; tokens that are not there are zeros
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = e4m3x2_to_f32x2(k[i] & 0xffffu), y = e4m3x2_to_f32x2(k[i] >> 16);
-        *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(x.x * sc, x.y * sc, y.x * sc, y.y * sc);
+    for (int i = 0; i < kMaxUnits; ++i) {
+      const int u = tid + i * kThreads;
+      if (u >= 2 * kTile * units) break;
+      const bool val = u >= kTile * units;
+      const int w = val ? u - kTile * units : u, j = (unsigned)w / (unsigned)units;
+      const uint32_t k[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+      const float sc = scl[i];
+      float* dst = (val ? sV : sK) + j * LD + (w - j * units) * 16;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 c0 = e4m3x2_to_f32x2(k[x] & 0xffffu), c1 = e4m3x2_to_f32x2(k[x] >> 16);
+        *reinterpret_cast<float4*>(dst + 4 * x) = make_float4(c0.x * sc, c0.y * sc, c1.x * sc, c1.y * sc);
       }
     }
+    if (ti + 1 < t1) fetch(ti + 1);
     __syncthreads();
     // scores and softmax: warp w takes heads w and w + 4, a lane a key
     const int t = base + lane;
     bool see = t < n && t >= first && (t < pre || (t <= p && t >= lo));
-    if (see && kv8_block(a.bt, a.cache.num_blocks, b, t / P) < 0) {
+    if (see && kv8_block(a.bt, a.cache.num_blocks, b, t >> shift) < 0) {
       record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
       see = false;
     }

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int B = a.bt.num_seqs, P = a.cache.rows_per_block, Hk = a.cache.kv_heads, G = a.group;
+  const int shift = 31 - __clz(P);
 
   // ---- the deal: exclusive prefix of the threads' segments of requests
   const int seg = (B + kThreads - 1) / kThreads;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
     auto block_of = [&](int s) {
       if (s >= steps) return -1;
       const int t0 = token0(s);
-      return t0 < n ? kv8_block(a.bt, a.cache.num_blocks, b, t0 / P) : -1;
+      return t0 < n ? kv8_block(a.bt, a.cache.num_blocks, b, t0 >> shift) : -1;
     };
     auto issue = [&](int s, int blk) {
       if (s < steps) {
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
     const bool cap = a.mask.softcap > 0.f, bias = a.mask.slopes != nullptr;
     const float pre_mul = cap ? 2.0f * kLog2e / a.mask.softcap : kLog2e, post_mul = a.mask.softcap * kLog2e;
 
-    float o[NB][C::kMb][4], m[NB][2], l[NB][2], vref = kKv8MinScale;
+    float o[NB][C::kMb][4], m[NB][2], l[NB][2], vref = kKv8MinScale, vinv = 1.0f / kKv8MinScale;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) raise |= sc[nb][i] > m[nb][i & 1] + kRescaleMargin;
+        for (int i = 0; i < 2; ++i) raise |= fmaxf(sc[nb][i], sc[nb][i + 2]) > m[nb][i] + kRescaleMargin;
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
       if (vscale > vref) {
         const float alpha = __fdividef(vref, vscale);
         vref = vscale;
+        vinv = 1.0f / vscale;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[nb][k][i] *= alpha;
       }
-      const float vr = vscale / vref;
+      const float vr = vscale * vinv;
       uint32_t pf[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {

@@ -2,51 +2,93 @@
 //
 // A block's scale is the largest of what it was and amax / 448 over its new rows, so a
 // (request, block, head, key or value) is one unit of work: one CTA reads the unit's rows
-// twice (amax, then the codes; the second time from L1), rounds the block's older rows
+// once (copies in shared memory last from amax to the codes; what does not fit there is
+// read again), rounds the block's older rows
 // again in the rare case that the scale rose, and no two CTAs meet at a scale.
 // HBM bounds it: 2 or 4 bytes in and 1 byte out a value.
 //
 // Units are found without a list.  With f(b) = row_start[b] / P + b, request b owns the
-// grid's x in [f(b), f(b+1)): the grid is n_rows / P + num_seqs wide, whatever the
-// lengths are, a request of n rows owns at least n / P + 1 of them and touches at most one
-// block more, which the owner of its first block takes too.
+// units x in [f(b), f(b+1)): there are n_rows / P + num_seqs, whatever the lengths are.  A
+// request of n rows owns at least n / P + 1 of them and touches at most one block more,
+// which the owner of its first block takes too.
+
+#include <algorithm>
 
 #include "csa_kernels.h"
 #include "kv8.cuh"
+#include "tc_ptx.cuh"
 
 namespace csa {
 namespace {
 
-constexpr int kThreads = 256;
+// Units of hundreds of rows keep 256 threads and 64 KB of copies busy, three CTAs an SM; those
+// of a few rows need neither.
+constexpr int kBigThreads = 256, kBigBytes = 65536;
+constexpr int kSmallThreads = 64, kSmallBytes = 4096;
+
+// 16 values as they are stored.
+template <typename T>
+struct Raw {
+  uint32_t w[4 * sizeof(T)];
+};
 
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, bool vec, float* v) {
+__device__ __forceinline__ Raw<T> load16(const T* p, bool vec) {
+  Raw<T> r;
   if (vec) {
-    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + j);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int j = 0; j < (int)sizeof(T); ++j) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + j);
+      r.w[4 * j] = x.x, r.w[4 * j + 1] = x.y, r.w[4 * j + 2] = x.z, r.w[4 * j + 3] = x.w;
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[8 * j + 2 * i] = __uint_as_float(u[i] << 16);
-          v[8 * j + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-      }
-    } else {
+    for (int j = 0; j < 8; ++j) r.w[j] = (uint32_t)h[2 * j] | (uint32_t)h[2 * j + 1] << 16;
+  } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(p) + j);
-        v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
-      }
+    for (int j = 0; j < 16; ++j) r.w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void values(const Raw<T>& r, float* v) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = __uint_as_float(r.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if constexpr (sizeof(T) == 2) v[i] = bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
-      else v[i] = p[i];
-    }
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r.w[i]);
   }
+}
+
+// The largest magnitude of 16 values, as the bits of a float.
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(const Raw<T>& r) {
+  uint32_t m = 0;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, r.w[i] & 0x7fff7fffu);
+    return max(m << 16, m & 0x7fff0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, r.w[i] & 0x7fffffffu);
+    return m;
+  }
+}
+
+// Block-wide maximum; red: a word for each warp.
+__device__ __forceinline__ uint32_t block_top(uint32_t v, uint32_t* red) {
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  v = __reduce_max_sync(0xffffffffu, v);
+  __syncthreads();
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, lane < nw ? red[lane] : 0u);
 }
 
 __device__ __forceinline__ uint4 pack16(const float* v, float mul) {
@@ -58,15 +100,17 @@ __device__ __forceinline__ uint4 pack16(const float* v, float mul) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T>
+template <typename T, int kThreads, int kBytes>
 __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs a) {
-  __shared__ float red[32];
+  extern __shared__ __align__(16) uint8_t buf[];
+  __shared__ uint32_t red[32];
   __shared__ int owner;
   pdl_trigger();
   pdl_wait();
   const int B = a.bt.num_seqs, P = a.cache.rows_per_block, Hk = a.cache.kv_heads, D = a.cache.dim;
-  const int tid = threadIdx.x, h = blockIdx.y;
-  const int64_t x = blockIdx.x;
+  // the heads' keys and values of one stretch of rows run together: they are neighbours in memory
+  const int tid = threadIdx.x, hv = blockIdx.x % (2 * Hk), h = hv % Hk;
+  const int64_t x = blockIdx.x / (2 * Hk);
   auto first_x = [&](int b) { return (int64_t)a.row_start[b] / P + b; };
   if (tid < 32) {
     const int b = warp_last_le(B, x, first_x);
@@ -78,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
   if (!kv8_request(a.row_start, a.cached, b, a.n_rows, a.bt, P, r, a.err) || r.rows() == 0) return;
   const int64_t x0 = first_x(b), owned = (int64_t)r.r1 / P + b + 1 - x0;
   if (x < x0 || x >= x0 + owned) return;
-  const bool val = blockIdx.z != 0;
+  const bool val = hv >= Hk;
   const T* src = reinterpret_cast<const T*>(a.x[val]) + (int64_t)h * D;
   const int64_t stride = a.stride[val];
   uint8_t* codes = reinterpret_cast<uint8_t*>(val ? a.cache.v : a.cache.k);
@@ -97,23 +141,53 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
     const int64_t at = (int64_t)blk * Hk + h;
     uint8_t* dst = codes + at * P * D;
     const float was = old ? scales[at] : 0.f;
-    float top = 0.f;
-    bool bad = false;
-#pragma unroll 4
-    for (int u = tid; u < m * units; u += kThreads) {
-      const int row = u / units;
-      float v[16];
-      load16(rows + row * stride + (u - row * units) * 16, a.vec, v);
+    // the thread's pieces (16 values): as many as fit are copied to shared memory and stay there
+    // between the two passes, 16 bytes of all pieces next to each other
+    constexpr int kKept = kBytes / (16 * (int)sizeof(T));
+    const int kept = a.vec ? min(m * units, kKept) : 0;
+    auto source = [&](int u) {
+      const int row = (unsigned)u / (unsigned)units;
+      return rows + row * stride + (u - row * units) * 16;
+    };
+    for (int u = tid; u < kept; u += kThreads) {
+      const T* src = source(u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float y = fabsf(v[i]);
-        const bool fin = y <= 3.402823466e38f;  // false for NaN
-        bad |= !fin;
-        top = fmaxf(top, fin ? y : 0.f);
-      }
+      for (int j = 0; j < (int)sizeof(T); ++j)
+        tc::cp_async16(tc::smem_u32(buf) + (j * kKept + u) * 16, reinterpret_cast<const uint4*>(src) + j, 16);
     }
-    top = block_max(top, red);
-    if (bad) record_error(a.err, CSA_ERR_NONFINITE);
+    tc::cp_async_commit();
+    auto piece = [&](int u) {
+      if (u >= kept) return load16(source(u), a.vec);
+      Raw<T> r;
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(T); ++j) {
+        const uint4 x = reinterpret_cast<const uint4*>(buf)[j * kKept + u];
+        r.w[4 * j] = x.x, r.w[4 * j + 1] = x.y, r.w[4 * j + 2] = x.z, r.w[4 * j + 3] = x.w;
+      }
+      return r;
+    };
+    tc::cp_async_wait<0>();  // a thread reads its own copies alone
+    // magnitudes order as their bits do; a NaN or an infinity lies at or above kInf
+    constexpr uint32_t kInf = 0x7f800000u;
+    uint32_t most = 0;
+    for (int u = tid; u < m * units; u += kThreads) most = max(most, top_bits(piece(u)));
+    most = block_top(most, red);
+    const bool odd = most >= kInf;
+    if (odd) {  // the largest finite one
+      if (tid == 0) record_error(a.err, CSA_ERR_NONFINITE);
+      most = 0;
+      for (int u = tid; u < m * units; u += kThreads) {
+        float v[16];
+        values(piece(u), v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t y = __float_as_uint(v[i]) & 0x7fffffffu;
+          most = y < kInf ? max(most, y) : most;
+        }
+      }
+      most = block_top(most, red);
+    }
+    const float top = __uint_as_float(most);
     const float scale = fmaxf(fmaxf(was, top * (1.0f / 448.0f)), kKv8MinScale);
     const float inv = 1.0f / scale;
     if (old && scale > was) {
@@ -131,26 +205,51 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
         *c = pack16(v, ratio);
       }
     }
-#pragma unroll 2
-    for (int u = tid; u < m * units; u += kThreads) {
-      const int row = u / units;
-      float v[16];
-      load16(rows + row * stride + (u - row * units) * 16, a.vec, v);
+    uint4* to = reinterpret_cast<uint4*>(dst) + (int64_t)old * units;
+    if (!odd) {
+      for (int u = tid; u < m * units; u += kThreads) {
+        float v[16];
+        values(piece(u), v);
+        to[u] = pack16(v, inv);
+      }
+    } else {
+      for (int u = tid; u < m * units; u += kThreads) {
+        float v[16];
+        values(piece(u), v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = v[i] == v[i] ? v[i] : 0.f;
-      reinterpret_cast<uint4*>(dst)[(int64_t)old * units + u] = pack16(v, inv);
+        for (int i = 0; i < 16; ++i) v[i] = v[i] == v[i] ? v[i] : 0.f;
+        to[u] = pack16(v, inv);
+      }
     }
-    if (tid == 0) scales[at] = scale;  // every thread has read it: block_max synchronises
+    if (tid == 0) scales[at] = scale;  // every thread has read it: block_top synchronises
   }
+}
+
+template <typename T, int kThreads, int kBytes>
+cudaError_t launch(const Kv8StoreArgs& a, cudaStream_t s) {
+  static PerDevice attr;
+  const cudaError_t e = with_device_slot(attr, [](int, int64_t& v) {
+    if (v) return cudaSuccess;
+    const cudaError_t err = cudaFuncSetAttribute(kv8_store_kernel<T, kThreads, kBytes>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (err == cudaSuccess) v = 1;
+    return err;
+  });
+  if (e != cudaSuccess) return e;
+  const unsigned gx = (unsigned)(a.n_rows / a.cache.rows_per_block + a.bt.num_seqs);
+  return launch_k(kv8_store_kernel<T, kThreads, kBytes>, dim3(gx * 2 * a.cache.kv_heads), dim3(kThreads), kBytes, s, 0, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_store(const Kv8StoreArgs& a, cudaStream_t s) {
-  const unsigned gx = (unsigned)(a.n_rows / a.cache.rows_per_block + a.bt.num_seqs);
-  const dim3 grid(gx, a.cache.kv_heads, 2);
-  if (a.in_dtype == CSA_F32) return launch_k(kv8_store_kernel<float>, grid, dim3(kThreads), 0, s, 0, a);
-  return launch_k(kv8_store_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, 0, a);
+  // rows of a unit, by the average request: up to a block's, or a step's few
+  const int32_t mean = a.n_rows / a.bt.num_seqs;
+  const bool small = std::min(mean, a.cache.rows_per_block) <= 16;
+  if (a.in_dtype == CSA_F32)
+    return small ? launch<float, kSmallThreads, kSmallBytes>(a, s) : launch<float, kBigThreads, kBigBytes>(a, s);
+  return small ? launch<__nv_bfloat16, kSmallThreads, kSmallBytes>(a, s)
+               : launch<__nv_bfloat16, kBigThreads, kBigBytes>(a, s);
 }
 
 }  // namespace csa

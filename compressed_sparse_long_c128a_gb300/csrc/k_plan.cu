@@ -31,11 +31,11 @@ __device__ __forceinline__ Req load_req(const PlanArgs& a, int b) {
   r.bad = c < 0 || n < 0 || (int64_t)c + n > INT32_MAX;
   r.cached = max(c, 0);
   r.n = r.bad ? 0 : n;
-  const int64_t P = a.block_positions;
-  const int64_t held = ((int64_t)r.cached + P - 1) / P, need = ((int64_t)r.cached + r.n + P - 1) / P;
-  r.bad |= need > a.stride;
-  r.held = (int32_t)min(held, (int64_t)a.stride);
-  r.take = (int32_t)(min(need, (int64_t)a.stride) - r.held);
+  const uint32_t P = a.block_positions;  // sums below 2^32
+  const uint32_t held = ((uint32_t)r.cached + P - 1) / P, need = ((uint32_t)r.cached + (uint32_t)r.n + P - 1) / P;
+  r.bad |= need > (uint32_t)a.stride;
+  r.held = (int32_t)min(held, (uint32_t)a.stride);
+  r.take = (int32_t)min(need, (uint32_t)a.stride) - r.held;
   return r;
 }
 
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
       o_seq[i] = b;
       o_pos[i] = p;
       if (a.slot) {
-        const int32_t l = p / a.block_positions;
+        const int32_t l = (uint32_t)p / (uint32_t)a.block_positions;
         if (l != lb) {
           lb = l;
           id = block_at(a, b, r, took, l);
@@ -166,6 +166,16 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
         }
         if (id >= 0) o_slot[i] = (int64_t)id * a.block_positions + (p - l * a.block_positions);
       }
+    }
+    if (a.vec && base + kRowsPerThread <= a.n_rows) {
+      *reinterpret_cast<int4*>(a.seq_id + base) = make_int4(o_seq[0], o_seq[1], o_seq[2], o_seq[3]);
+      *reinterpret_cast<int4*>(a.pos + base) = make_int4(o_pos[0], o_pos[1], o_pos[2], o_pos[3]);
+      if (a.slot) {
+        longlong2* dst = reinterpret_cast<longlong2*>(a.slot + base);
+        dst[0] = make_longlong2(o_slot[0], o_slot[1]);
+        dst[1] = make_longlong2(o_slot[2], o_slot[3]);
+      }
+      continue;
     }
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
