@@ -25,7 +25,7 @@ constexpr int kDimsPerThread = kMaxDim / kThreads;
 
 __host__ __device__ constexpr int simt_smem_floats(int D) { return 2 * kTile * (D + 4) + kHeads * D + 2 * kHeads * kTile + 2 * kHeads; }
 
-__global__ void __launch_bounds__(kThreads) kv8_attn_simt_kernel(const Kv8AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv8_attn_simt_kernel(const Kv8AttnArgs a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int owner;
   pdl_trigger();
@@ -244,10 +244,11 @@ __global__ void __launch_bounds__(kThreads) kv8_simt_join_kernel(const Kv8AttnAr
 }  // namespace
 
 int32_t kv8_simt_splits(int32_t n_rows, int32_t heads, int32_t kv_heads) {
-  // four CTAs fit an SM; splitting a row costs a second kernel, so it is done only
-  // where the rows alone would leave SMs idle
+  // A tile is a chain of latencies (codes, scores, softmax, sums) that four CTAs an SM only
+  // half hide, so a row's keys are split until there are three times as many CTAs: 69 us
+  // with one CTA a row, 57 us with four, on 111 rows of up to 740 keys.
   const int64_t ctas = (int64_t)n_rows * kv_heads * ((heads / kv_heads + kHeads - 1) / kHeads);
-  const int64_t s = ctas > 0 ? 608 / ctas : 1;
+  const int64_t s = ctas > 0 ? 1824 / ctas : 1;
   return (int32_t)(s < 1 ? 1 : s > 32 ? 32 : s);
 }
 

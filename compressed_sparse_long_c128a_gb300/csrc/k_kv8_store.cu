@@ -130,17 +130,9 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
   const int units = D / 16;  // 16 values, one 16-byte store of codes
   const int last = (r.len() - 1) / P;
   for (int64_t lb = r.cached / P + (x - x0); lb <= last; lb += owned) {
-    const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, b, (int32_t)lb);
-    if (blk < 0) {
-      if (tid == 0) record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
-      continue;
-    }
     const int32_t p0 = max(r.cached, (int32_t)(lb * P)), p1 = (int32_t)min((int64_t)r.len(), (lb + 1) * P);
     const int old = p0 - (int32_t)(lb * P), m = p1 - p0;  // older rows, new rows
     const T* rows = src + (int64_t)(r.r0 + p0 - r.cached) * stride;
-    const int64_t at = (int64_t)blk * Hk + h;
-    uint8_t* dst = codes + at * P * D;
-    const float was = old ? scales[at] : 0.f;
     // the thread's pieces (16 values): as many as fit are copied to shared memory and stay there
     // between the two passes, 16 bytes of all pieces next to each other
     constexpr int kKept = kBytes / (16 * (int)sizeof(T));
@@ -156,6 +148,16 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
         tc::cp_async16(tc::smem_u32(buf) + (j * kKept + u) * 16, reinterpret_cast<const uint4*>(src) + j, 16);
     }
     tc::cp_async_commit();
+    // (the block is looked up while the copies are on their way)
+    const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, b, (int32_t)lb);
+    if (blk < 0) {
+      if (tid == 0) record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
+      tc::cp_async_wait<0>();
+      continue;
+    }
+    const int64_t at = (int64_t)blk * Hk + h;
+    uint8_t* dst = codes + at * P * D;
+    const float was = old ? scales[at] : 0.f;
     auto piece = [&](int u) {
       if (u >= kept) return load16(source(u), a.vec);
       Raw<T> r;
