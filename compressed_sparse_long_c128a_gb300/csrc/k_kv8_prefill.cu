@@ -26,6 +26,7 @@
 //    divided out of each 16 columns' part of the sum.
 
 #include <cfloat>
+#include <type_traits>
 
 #include "csa_kernels.h"
 #include "kv8.cuh"
@@ -421,6 +422,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     // the cap rises with the accumulator: without a bias only the maximum is capped here (one over
     // hidden keys alone gives -cap, at or below every score)
     float mt = -INFINITY;
+    bool small = CAP && !BIAS;  // scores of at most the cap in magnitude, before it
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float* y = x + 16 * g;
@@ -429,7 +431,14 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
       for (int k = 0; k < 4; ++k) z[k] = fmaxf(fmaxf(y[k], y[k + 4]), fmaxf(y[k + 8], y[k + 12]));
       const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
       mt = fmaxf(mt, BIAS ? top : CAP ? post * tanh_exp2(top * f[g]) : top * f[g]);
+      if constexpr (CAP && !BIAS) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = fminf(fminf(y[k], y[k + 4]), fminf(y[k + 8], y[k + 12]));
+        const float low = fminf(fminf(z[0], z[1]), fminf(z[2], z[3]));
+        small &= fmaxf(top, -low) * f[g] <= 2.0f * kLog2e;
+      }
     }
+    small = CAP && !BIAS && __all_sync(0xffffffffu, small);
     if (__any_sync(0xffffffffu, mt > m + kRescaleMargin)) {
       const float mn = fmaxf(m, mt), alpha = fast_exp2(m - mn);
       m = mn;
@@ -451,37 +460,49 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     }
     // ---- P over S
     const float shift = kPShift - m;
+    auto write_p = [&](auto how) {  // 0: scores; 1: scores before the cap; 2: the same, all small
+      constexpr int kHow = decltype(how)::value;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const float add = shift + ms.lv[sb][g];
-      const float* y = x + 16 * g;
-      float2 sum = make_float2(0.f, 0.f);
-      uint32_t pw[8];
+      for (int g = 0; g < kGroups; ++g) {
+        const float add = shift + ms.lv[sb][g];
+        const float* y = x + 16 * g;
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t pw[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float2 e = make_float2(y[2 * k], y[2 * k + 1]);
-        if constexpr (BIAS) {
-          e = add2(e, make_float2(add, add));
-        } else if constexpr (CAP) {  // post tanh + add
-          e = make_float2(fast_exp2(e.x * f[g]), fast_exp2(e.y * f[g]));
-          e = add2(e, make_float2(1.f, 1.f));
-          e = make_float2(fast_rcp(e.x), fast_rcp(e.y));
-          e = fma2(e, make_float2(-2.f * post, -2.f * post), make_float2(post + add, post + add));
-        } else {
-          e = fma2(e, make_float2(f[g], f[g]), make_float2(add, add));
-        }
-        e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-        if constexpr (CAP && !BIAS) {  // -inf does not pass the cap
-          if (!plain) {
-            e.x = see >> (16 * g + 2 * k) & 1 ? e.x : 0.f;
-            e.y = see >> (16 * g + 2 * k + 1) & 1 ? e.y : 0.f;
+        for (int k = 0; k < 8; ++k) {
+          float2 e = make_float2(y[2 * k], y[2 * k + 1]);
+          if constexpr (BIAS) {
+            e = add2(e, make_float2(add, add));
+          } else if constexpr (kHow == 2) {
+            const float fu = f[g] * (0.5f / kLog2e);
+            e = fma2(tanh_small2(mul2(e, make_float2(fu, fu))), make_float2(post, post), make_float2(add, add));
+          } else if constexpr (kHow == 1) {  // post tanh + add
+            e = make_float2(fast_exp2(e.x * f[g]), fast_exp2(e.y * f[g]));
+            e = add2(e, make_float2(1.f, 1.f));
+            e = make_float2(fast_rcp(e.x), fast_rcp(e.y));
+            e = fma2(e, make_float2(-2.f * post, -2.f * post), make_float2(post + add, post + add));
+          } else {
+            e = fma2(e, make_float2(f[g], f[g]), make_float2(add, add));
           }
+          e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+          if constexpr (kHow == 1) {  // -inf does not pass the cap
+            if (!plain) {
+              e.x = see >> (16 * g + 2 * k) & 1 ? e.x : 0.f;
+              e.y = see >> (16 * g + 2 * k + 1) & 1 ? e.y : 0.f;
+            }
+          }
+          sum = k ? add2(sum, e) : e;
+          pw[k] = f32x2_to_f16x2(e.x, e.y);
         }
-        sum = k ? add2(sum, e) : e;
-        pw[k] = f32x2_to_f16x2(e.x, e.y);
+        l = fmaf(sum.x + sum.y, ms.rv[sb][g], l);
+        tmem_st8(s_addr + 8 * g, pw);
       }
-      l = fmaf(sum.x + sum.y, ms.rv[sb][g], l);
-      tmem_st8(s_addr + 8 * g, pw);
+    };
+    if constexpr (CAP && !BIAS) {
+      if (small) write_p(std::integral_constant<int, 2>{});
+      else write_p(std::integral_constant<int, 1>{});
+    } else {
+      write_p(std::integral_constant<int, 0>{});
     }
     tmem_wait_st();
     tc_fence_before();
