@@ -72,7 +72,10 @@ struct Misc {
   // of the last tiles, by 16 tokens: offset of the codes (-1: none), key scale (negative: no block),
   // log2 of the value scale relative to v_max, and its inverse
   int64_t src[2 * kPairBufs][kGroups];
-  float ks[2 * kPairBufs][kGroups], lv[2 * kPairBufs][kGroups], rv[2 * kPairBufs][kGroups];
+  alignas(16) float ks[2 * kPairBufs][kGroups];
+  alignas(16) float lv[2 * kPairBufs][kGroups];
+  alignas(16) float rv[2 * kPairBufs][kGroups];
+  int32_t plain[2 * kPairBufs];  // every row of the CTA sees every key of the tile
 };
 
 template <int D>
@@ -94,6 +97,7 @@ struct Part {
   Kv8Req r;
   int32_t b, kvh, i0, tpt;  // tpt: tokens of a query tile
   int32_t n, first, pre;    // tokens stored, the lowest document start, the prefix
+  int32_t all_first, all_lo, all_p;  // what all rows have in common: see from here on, to here
   Kv8Tiles tiles;
   int32_t count;            // key tiles
 };
@@ -242,6 +246,13 @@ __device__ void look_up_role(const Kv8AttnArgs& a, const Part& w, Misc& ms) {
       ms.lv[sb][g] = log2f(vs);
       ms.rv[sb][g] = 1.0f / vs;
     }
+    // of the four lanes of a tile: all of its tokens are there, and no row's mask cuts it
+    const uint32_t there = __ballot_sync(0xffffffffu, src >= 0);
+    if (t < w.count && g == 0) {
+      const int t0 = w.tiles.at(t) * kTile;
+      ms.plain[sb] = (there >> lane & 15u) == 15u && t0 + kTile <= w.n && t0 >= w.all_first &&
+                     ((t0 >= w.all_lo && t0 + kTile - 1 <= w.all_p) || t0 + kTile <= w.pre);
+    }
     __syncwarp();
     if (lane == 0)
       for (int u = u0; u < u0 + 4 && 2 * u < w.count; ++u) mbar_arrive(&ms.at_full[u % kPairBufs]);
@@ -371,7 +382,6 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
   const float fac = p2 * a.mask.scale * (CAP ? 2.0f * kLog2e / a.mask.softcap : kLog2e);
   const float post = a.mask.softcap * kLog2e;
   const float slope = BIAS && real ? a.mask.slopes[head] * kLog2e : 0.f;
-  // rows that do not exist see every key, so that they ask for no mask
   const int p = real ? w.r.cached + tok : INT32_MAX;
   const int first = real && a.mask.first ? max(0, a.mask.first[row]) : 0;
   const int lo = real && a.mask.window > 0 ? max(first, p - a.mask.window + 1) : first;
@@ -385,16 +395,10 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     wait_or_abort(ms, &ms.at_full[u % kPairBufs], (u / kPairBufs) & 1, a.err);
     // what turns the accumulator's 16 columns into scores in log2 units, before the cap; not 0, so
     // that it leaves -inf alone
-    float f[kGroups];
-    bool mapped = true;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const float ks = ms.ks[sb][g];
-      mapped &= ks >= 0.f;
-      f[g] = fmaxf(fac * ks, FLT_MIN);
-    }
-    const bool whole = t0 >= first && t0 + kTile <= w.n && ((t0 >= lo && t0 + kTile - 1 <= p) || t0 + kTile <= w.pre);
-    const bool plain = __all_sync(0xffffffffu, whole && mapped);
+    const float4 ks4 = *reinterpret_cast<const float4*>(ms.ks[sb]);
+    const float f[kGroups] = {fmaxf(fac * ks4.x, FLT_MIN), fmaxf(fac * ks4.y, FLT_MIN), fmaxf(fac * ks4.z, FLT_MIN),
+                              fmaxf(fac * ks4.w, FLT_MIN)};
+    const bool plain = ms.plain[sb];
     wait_or_abort(ms, &ms.s_full[i][t & 1], u & 1, a.err);
     tc_fence_after();
     float x[kTile];
@@ -459,12 +463,14 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
       }
     }
     // ---- P over S
+    const float4 lv4 = *reinterpret_cast<const float4*>(ms.lv[sb]), rv4 = *reinterpret_cast<const float4*>(ms.rv[sb]);
+    const float lv[kGroups] = {lv4.x, lv4.y, lv4.z, lv4.w}, rv[kGroups] = {rv4.x, rv4.y, rv4.z, rv4.w};
     const float shift = kPShift - m;
     auto write_p = [&](auto how) {  // 0: scores; 1: scores before the cap; 2: the same, all small
       constexpr int kHow = decltype(how)::value;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const float add = shift + ms.lv[sb][g];
+        const float add = shift + lv[g];
         const float* y = x + 16 * g;
         float2 sum = make_float2(0.f, 0.f);
         uint32_t pw[8];
@@ -494,7 +500,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
           sum = k ? add2(sum, e) : e;
           pw[k] = f32x2_to_f16x2(e.x, e.y);
         }
-        l = fmaf(sum.x + sum.y, ms.rv[sb][g], l);
+        l = fmaf(sum.x + sum.y, rv[g], l);
         tmem_st8(s_addr + 8 * g, pw);
       }
     };
@@ -599,9 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
   w.pre = a.mask.prefix ? min(a.mask.prefix[w.b], w.n) : 0;
   if (a.mask.first) {
     w.first = INT32_MAX;
-    for (int i = w.i0; i <= last; ++i) w.first = min(w.first, a.mask.first[w.r.r0 + i]);
-    w.first = max(w.first, 0);
+    for (int i = w.i0; i <= last; ++i) {
+      const int32_t f = max(a.mask.first[w.r.r0 + i], 0);
+      w.first = min(w.first, f);
+      w.all_first = max(w.all_first, f);
+    }
   }
+  w.all_p = w.r.cached + w.i0;
+  w.all_lo = a.mask.window > 0 ? max(w.all_first, w.r.cached + last - a.mask.window + 1) : w.all_first;
   const int lo = a.mask.window > 0 ? max(w.first, w.r.cached + w.i0 - a.mask.window + 1) : w.first;
   w.tiles = kv8_tiles(kTile, w.first, w.pre, lo, w.r.cached + last);
   w.count = w.tiles.count();
