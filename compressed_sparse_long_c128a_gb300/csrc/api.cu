@@ -2,6 +2,7 @@
 // entry point validates on the host, enqueues its kernels on the caller's
 // stream and returns without synchronising or allocating.
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -50,11 +51,10 @@ struct Kv8Plan {
   int32_t cols, few_cols;
   bool many;
 };
-Kv8Plan kv8_plan(int32_t n_rows, int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t dim, int32_t max_new) {
-  const int32_t group = heads / kv_heads;
+Kv8Plan kv8_plan(int32_t group, int32_t max_new) {
   const int64_t most = (int64_t)group * max_new;
   Kv8Plan p{most > 32 ? 32 : (int32_t)most, INT32_MAX, false};
-  if (most <= 32 || !kv8_prefill_eligible(dim, group)) return p;
+  if (most <= 32 || !kv8_prefill_eligible(group)) return p;
   // requests of single tokens among long ones keep tiles of their own width
   p.many = true;
   p.few_cols = 32;
@@ -451,15 +451,16 @@ size_t csa_kv8_attn_workspace_size(int32_t n_rows, int32_t num_seqs, int32_t hea
                                    int32_t max_new) {
   if (!cache || n_rows <= 0 || num_seqs <= 0 || heads <= 0 || cache->kv_heads <= 0 || cache->dim <= 0 || max_new <= 0)
     return 0;
-  // the query type decides between the kernels; size for the larger
-  const size_t simt =
-      kv8_simt_workspace(n_rows, heads, cache->dim, kv8_simt_splits(n_rows, heads, cache->kv_heads));
-  const size_t tc = kv8_decode_eligible(CSA_BF16, CSA_BF16, cache->dim)
-                        ? kv8_decode_workspace(
-                              cache->dim,
-                              kv8_plan(n_rows, num_seqs, heads, cache->kv_heads, cache->dim, max_new).cols)
-                        : 0;
-  return align_up(simt > tc ? simt : tc);
+  // the types decide between the kernels, which run one after the other; size for the largest
+  const int32_t kv = cache->kv_heads, dim = cache->dim;
+  if (heads < kv) return 0;
+  const Kv8Plan p = kv8_plan(heads / kv, max_new);
+  size_t most = std::max(kv8_simt_workspace(n_rows, heads, dim, kv8_simt_splits(n_rows, heads, kv)),
+                         kv8_decode_workspace(dim, p.cols));
+  if (p.many)
+    most = std::max(most, kv8_prefill_workspace(n_rows, num_seqs, heads, kv, dim,
+                                                kv8_prefill_splits(n_rows, num_seqs, heads, kv, dim, INT64_MAX)));
+  return align_up(most);
 }
 
 int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_rows, int32_t heads,
@@ -476,7 +477,7 @@ int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_row
   if ((st = check_bt(bt))) return st;
   if (heads % cache->kv_heads) return CSA_ERR_INVALID_ARG;
   if (!(mask->scale > 0.f) || !std::isfinite(mask->scale) || !(mask->softcap >= 0.f) || !std::isfinite(mask->softcap) ||
-      mask->window < 0)
+      (mask->softcap > 0.f && mask->softcap < 5.421010862427522e-20f) || mask->window < 0)
     return CSA_ERR_INVALID_ARG;
   if (heads > 65535) return CSA_ERR_UNSUPPORTED;
   const size_t q_el = q_dtype == CSA_F32 ? 4 : 2, o_el = out_dtype == CSA_F32 ? 4 : 2;
@@ -500,15 +501,19 @@ int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_row
   a.out_dtype = out_dtype;
   a.lse = lse;
   a.err = err;
-  if (kv8_decode_eligible(q_dtype, out_dtype, cache->dim)) {
+  if (q_dtype == CSA_BF16 && out_dtype == CSA_BF16) {
     a.q_vec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_stride % 8 == 0;
     a.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    const Kv8Plan p = kv8_plan(n_rows, bt->num_seqs, heads, cache->kv_heads, cache->dim, max_new);
+    const Kv8Plan p = kv8_plan(a.group, max_new);
     a.cols = p.cols;
     a.few_cols = p.few_cols;
     kv8_decode_parts(a, ws);
     if (launch_kv8_decode(a, stream) != cudaSuccess) return CSA_ERR_CUDA;
-    return p.many ? cuda_status(launch_kv8_prefill(a, stream)) : CSA_OK;
+    if (!p.many) return CSA_OK;
+    a.n_splits = kv8_prefill_splits(n_rows, bt->num_seqs, heads, cache->kv_heads, cache->dim,
+                                    (int64_t)bt->stride * cache->rows_per_block);
+    kv8_prefill_parts(a, ws);
+    return cuda_status(launch_kv8_prefill(a, stream));
   }
   a.n_splits = kv8_simt_splits(n_rows, heads, cache->kv_heads);
   a.part_o = reinterpret_cast<float*>(ws);

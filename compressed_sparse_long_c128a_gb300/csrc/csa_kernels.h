@@ -322,17 +322,21 @@ struct Kv8AttnArgs {
   int32_t q_vec, out_vec;  // q rows and out may be accessed 16 bytes at a time
   int32_t* err;
 };
-// CUDA-core kernel, any type and dim: splits of a row's keys, and its scratch
+// CUDA-core kernel, any type: splits of a row's keys, and its scratch
 int32_t kv8_simt_splits(int32_t n_rows, int32_t heads, int32_t kv_heads);
 size_t kv8_simt_workspace(int32_t n_rows, int32_t heads, int32_t dim, int32_t n_splits);
 cudaError_t launch_kv8_attn_simt(const Kv8AttnArgs& a, cudaStream_t s);
-// few rows a request, bf16 queries, dims 64, 128, 256 (k_kv8_decode.cu)
-bool kv8_decode_eligible(int32_t q_dtype, int32_t out_dtype, int32_t dim);
+// bf16 in and out: requests of few rows (k_kv8_decode.cu) ...
 size_t kv8_decode_workspace(int32_t dim, int32_t cols);
 void kv8_decode_parts(Kv8AttnArgs& a, void* ws);  // the workspace's parts, for a.cols columns
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t s);
-// many rows a request: those of more than few_cols columns (k_kv8_prefill.cu)
-bool kv8_prefill_eligible(int32_t dim, int32_t group);
+// ... and those of more than few_cols columns (k_kv8_prefill.cu)
+bool kv8_prefill_eligible(int32_t group);
+int32_t kv8_prefill_splits(int32_t n_rows, int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t dim,
+                           int64_t max_len);
+size_t kv8_prefill_workspace(int32_t n_rows, int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t dim,
+                             int32_t splits);
+void kv8_prefill_parts(Kv8AttnArgs& a, void* ws);  // for a.n_splits
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s);
 
 }  // namespace csa

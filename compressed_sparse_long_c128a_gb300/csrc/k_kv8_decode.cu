@@ -1,5 +1,6 @@
 // Attention of few rows a request over the 8-bit key / value cache: single tokens and
-// short runs of them, bf16 queries and results, heads of 64, 128 or 256.
+// short runs of them, bf16 queries and results.  D is the head size, rounded up to 64, 128
+// or 256; the dims past it are zeros that are never read or written.
 //
 // Every key and value is read once and meets 8 to 32 query columns (rows x query heads
 // of a key head), so HBM bounds it: 2 D bytes a token and key head.  What it takes is
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int B = a.bt.num_seqs, P = a.cache.rows_per_block, Hk = a.cache.kv_heads, G = a.group;
-  const int shift = 31 - __clz(P);
+  const int shift = 31 - __clz(P), dim = a.cache.dim;
 
   // ---- the deal: exclusive prefix of the threads' segments of requests
   const int seg = (B + kThreads - 1) / kThreads;
@@ -207,18 +208,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
         const int st = s % ST, t0 = token0(s);
         const int left = blk >= 0 ? n - t0 : 0;  // tokens there are
         const int64_t at = (int64_t)max(blk, 0) * Hk + kvh;
-        const int64_t off = (at * P + (t0 & (P - 1))) * D;
+        const int64_t off = (at * P + (t0 & (P - 1))) * dim;
         const uint8_t* ks = reinterpret_cast<const uint8_t*>(a.cache.k) + off;
         const uint8_t* vs = reinterpret_cast<const uint8_t*>(a.cache.v) + off;
         const uint32_t dst = my_ring + st * C::kStageBytes;
 #pragma unroll
         for (int i = 0; i < CH / 2; ++i) {
           const int x = lane + 32 * i, r = x / CH, c = x % CH;
-          const bool there = r < left;  // else zeros are written and nothing is read
+          const bool there = r < left && c * 16 < dim;  // else zeros are written and nothing is read
+          const int from = r * dim + c * 16;
           tc::cp_async16(dst + piece_offset<D, false>(r, c),
-                         there ? ks + x * 16 : reinterpret_cast<const uint8_t*>(a.cache.k), there ? 16u : 0u);
+                         there ? ks + from : reinterpret_cast<const uint8_t*>(a.cache.k), there ? 16u : 0u);
           tc::cp_async16(dst + kStep * D + piece_offset<D, true>(r, c),
-                         there ? vs + x * 16 : reinterpret_cast<const uint8_t*>(a.cache.v), there ? 16u : 0u);
+                         there ? vs + from : reinterpret_cast<const uint8_t*>(a.cache.v), there ? 16u : 0u);
         }
         if (lane < 2) {
           if (blk >= 0) {
@@ -261,15 +263,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int col = nb * 8 + g;
-      const bool real = col < n_cols;
+      const bool col_there = col < n_cols;
       const int cg = min(col0 + col, n_rows * G - 1);
       const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(job.r.r0 + cg / G) * a.q_stride +
-                          (int64_t)(kvh * G + cg % G) * D;
+                          (int64_t)(kvh * G + cg % G) * dim;
       float top = 0.f;
 #pragma unroll
       for (int j = 0; j < CH / 4; ++j) {
         uint32_t w[8];
-        const uint16_t* src = q + (t4 + 4 * j) * 16;
+        const bool real = col_there && (t4 + 4 * j) * 16 < dim;
+        const uint16_t* src = q + (real ? (t4 + 4 * j) * 16 : 0);
         if (a.q_vec) {
           const uint4 x = __ldg(reinterpret_cast<const uint4*>(src)), y = __ldg(reinterpret_cast<const uint4*>(src) + 1);
           w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
@@ -355,11 +358,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[nb][i] *= fac[nb][i & 1] * mul;
       if (cap) {
+        bool small = true;  // of at most the cap in magnitude: 9e-8 of themselves off, not of the cap
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) small &= fabsf(sc[nb][i]) <= 2.0f * kLog2e;
+        small = __all_sync(0xffffffffu, small);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           if (nb >= nbs) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[nb][i] = post_mul * tanh_exp2(sc[nb][i]);
+          for (int i = 0; i < 4; i += 2) {
+            const float2 y = make_float2(sc[nb][i], sc[nb][i + 1]);
+            const float2 z = small ? tanh_small2(mul2(y, make_float2(0.5f / kLog2e, 0.5f / kLog2e)))
+                                   : make_float2(tanh_exp2(y.x), tanh_exp2(y.y));
+            sc[nb][i] = post_mul * z.x;
+            sc[nb][i + 1] = post_mul * z.y;
+          }
         }
       }
       if (bias) {
@@ -523,11 +538,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
           y[2 * k + e] = v;
         }
       const int d0 = D == 256 ? half * 128 + 16 * g : (D / 8) * g + half * (D / 16);
-      if (c < n_cols && whole_pair) {
+      if (d0 >= dim) {
+      } else if (c < n_cols && whole_pair) {
         const int cg = col0 + c;
         const int64_t rh = (int64_t)(job.r.r0 + cg / G) * a.heads + kvh * G + cg % G;
         const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + rh * D + d0;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + rh * dim + d0;
         uint32_t z[kHalf];
 #pragma unroll
         for (int k = 0; k < kHalf; ++k) z[k] = f32x2_to_bf16x2(y[2 * k] * inv, y[2 * k + 1] * inv);
@@ -607,7 +623,7 @@ __global__ void __launch_bounds__(kThreads) kv8_decode_join_kernel(const Kv8Attn
   __syncthreads();
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   for (int d = tid; d < D; d += kThreads)
-    reinterpret_cast<uint16_t*>(a.out)[rh * D + d] =
+    if (d < a.cache.dim) reinterpret_cast<uint16_t*>(a.out)[rh * a.cache.dim + d] =
         f32_to_bf16(((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) * inv);
   if (a.lse && tid == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
 }
@@ -632,9 +648,9 @@ cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t s) {
 
 template <typename F>
 auto pick(int32_t dim, int32_t cols, F f) {
-  if (dim == 64)
+  if (dim <= 64)
     return cols <= 8 ? f.template run<64, 1>() : cols <= 16 ? f.template run<64, 2>() : f.template run<64, 4>();
-  if (dim == 128)
+  if (dim <= 128)
     return cols <= 8 ? f.template run<128, 1>() : cols <= 16 ? f.template run<128, 2>() : f.template run<128, 4>();
   return cols <= 8 ? f.template run<256, 1>() : f.template run<256, 2>();  // wider tiles exceed the registers
 }
@@ -652,20 +668,18 @@ struct Launch {
 
 }  // namespace
 
-bool kv8_decode_eligible(int32_t q_dtype, int32_t out_dtype, int32_t dim) {
-  return q_dtype == CSA_BF16 && out_dtype == CSA_BF16 && (dim == 64 || dim == 128 || dim == 256);
-}
-
 // O of every slot's columns, (max, sum) of each, then 8 words a CTA (fewer than the slots).
+static int32_t tile_dim(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
 size_t kv8_decode_workspace(int32_t dim, int32_t cols) {
   const size_t slots = pick(dim, cols, SlotsOf{});
-  return slots * dim * sizeof(float) + slots * 2 * sizeof(float) + slots * 8 * sizeof(int32_t) / 2;
+  return slots * tile_dim(dim) * sizeof(float) + slots * 2 * sizeof(float) + slots * 8 * sizeof(int32_t) / 2;
 }
 
 void kv8_decode_parts(Kv8AttnArgs& a, void* ws) {
   const size_t slots = pick(a.cache.dim, a.cols, SlotsOf{});
   a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = a.part_o + slots * a.cache.dim;
+  a.part_ml = a.part_o + slots * tile_dim(a.cache.dim);
   a.part_head = reinterpret_cast<int32_t*>(a.part_ml + slots * 2);
 }
 

@@ -39,9 +39,8 @@ using namespace tc;
 
 constexpr int kTile = 64;      // keys of a tile
 constexpr int kM = 128;        // rows of a query tile
-constexpr int kMTiles = 2;
-constexpr int kStages = 2;     // pairs of key tiles, and of value tiles, in shared memory
-constexpr int kSoftmax = kMTiles * 128, kConvert = 128;
+constexpr int kStages = 2;     // of key tiles, and of value tiles, in shared memory
+constexpr int kSoftmax = 256, kConvert = 128;
 constexpr int kThreads = kSoftmax + kConvert + 64;
 constexpr int kMmaWarp = (kSoftmax + kConvert) / 32, kLookWarp = kMmaWarp + 1;
 constexpr int kGroups = kTile / 16;  // tokens that share a scale
@@ -49,20 +48,23 @@ constexpr int kPairBufs = 8;         // pairs of tiles whose addresses and scale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleMargin = 8.0f, kPShift = 7.0f;
 
+// D: the head size, rounded up to 64, 128 or 256 (the rest are zeros)
 template <int D>
 struct Cfg {
+  static constexpr int kMT = D == 256 ? 1 : 2;   // query tiles: O takes kMT D columns of TMEM
+  static constexpr int kPer = D == 256 ? 1 : 2;  // tiles of a stage, as shared memory allows
   static constexpr uint32_t kQAtom = kM * 128, kAtom = kTile * 128;  // rows of 64 f16
   static constexpr uint32_t kQBytes = kQAtom * (D / 64), kTileBytes = kAtom * (D / 64);
-  static constexpr uint32_t kOffK = kMTiles * kQBytes, kOffV = kOffK + 2 * kStages * kTileBytes;
-  static constexpr uint32_t kOffMisc = kOffV + 2 * kStages * kTileBytes;
-  static constexpr uint32_t kColO = kMTiles * 2 * kTile;      // S_i(t) at (2 i + t % 2) kTile
+  static constexpr uint32_t kOffK = kMT * kQBytes, kOffV = kOffK + kPer * kStages * kTileBytes;
+  static constexpr uint32_t kOffMisc = kOffV + kPer * kStages * kTileBytes;
+  static constexpr uint32_t kColO = kMT * 2 * kTile;          // S_i(t) at (2 i + t % 2) kTile
   static constexpr int kUnits = kTile * (D / 16) / kConvert;  // 16-byte pieces of a tile a thread
 };
 
 struct Misc {
   uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
   // by the parity of t: who waits for a tile may be one tile behind, never two
-  uint64_t s_full[kMTiles][2], p_full[kMTiles][2], o_done[kMTiles][2];
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
   uint64_t at_full[kPairBufs], at_free[kPairBufs], q_full, mma_done;
   uint32_t tmem_base;
   int32_t abort;
@@ -95,11 +97,12 @@ __device__ __forceinline__ bool wait_or_abort(Misc& ms, uint64_t* bar, uint32_t 
 // What a CTA works on: tokens [i0, i0 + nt) of request b for key head kvh.
 struct Part {
   Kv8Req r;
-  int32_t b, kvh, i0, tpt;  // tpt: tokens of a query tile
+  int32_t b, kvh, x, i0, tpt;  // x: of the grid; tpt: tokens of a query tile
   int32_t n, first, pre;    // tokens stored, the lowest document start, the prefix
   int32_t all_first, all_lo, all_p;  // what all rows have in common: see from here on, to here
   Kv8Tiles tiles;
-  int32_t count;            // key tiles
+  int32_t begin, count;     // of the key tiles: this CTA's share
+  __device__ __forceinline__ int32_t tile(int32_t t) const { return tiles.at(begin + t); }
 };
 
 // ------------------------------------------------------------------ conversion
@@ -110,22 +113,24 @@ template <int D>
 struct Unit {
   int row, piece;  // row: of the thread's first unit, the others kConvert 16 / D further each
   __device__ __forceinline__ explicit Unit(int ct) {
-    if constexpr (D == 64) {
+    if constexpr (D == 64) {  // 32 rows of 4 pieces
       row = ct >> 2, piece = ct & 3;
-    } else {
+    } else if constexpr (D == 128) {  // 16 rows of 8
       row = ((ct >> 2) & 1) + 2 * (ct >> 4), piece = (ct & 3) + ((ct >> 1) & 4);
+    } else {  // 8 rows of 16
+      row = ((ct >> 2) & 1) + 2 * (ct >> 5), piece = (ct & 3) + ((ct >> 1) & 12);
     }
   }
 };
 
 template <int D>
-__device__ __forceinline__ void load_units(const int64_t* src, const uint8_t* codes, const Unit<D>& un, uint4* x) {
+__device__ __forceinline__ void load_units(const int64_t* src, const uint8_t* codes, int dim, const Unit<D>& un, uint4* x) {
   constexpr int kRows = kConvert / (D / 16);
 #pragma unroll
   for (int i = 0; i < Cfg<D>::kUnits; ++i) {
     const int row = un.row + i * kRows;
-    const int64_t at = src[row / 16];  // tokens past the sequence hold some code: only V needs zeros there
-    x[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at + (row % 16) * D + un.piece * 16))
+    const int64_t at = un.piece * 16 < dim ? src[row / 16] : -1;  // tokens past the sequence hold any code
+    x[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at + (row % 16) * dim + un.piece * 16))
                    : make_uint4(0, 0, 0, 0);
   }
 }
@@ -158,7 +163,8 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   // the largest value scale of the blocks that the tiles touch
   float top = kKv8MinScale;
   for (int part = 0; part < 2; ++part) {
-    const int t0 = (part ? w.tiles.tB : w.tiles.tA) * kTile, nt = part ? w.tiles.nB : w.tiles.nA;
+    const int i0 = part ? max(w.begin, w.tiles.nA) : w.begin;
+    const int nt = (part ? w.begin + w.count : min(w.begin + w.count, w.tiles.nA)) - i0, t0 = w.tiles.at(i0) * kTile;
     const int lb1 = (min(w.n, t0 + nt * kTile) + P - 1) >> shift;
     if (nt > 0)
 #pragma unroll 4
@@ -175,22 +181,24 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   if (ct == 0) ms.v_max = top;
   named_bar(2, kConvert + 32);  // for the look-up warp, which passes it on
   const Unit<D> un(ct);
-  uint4 kx[2][C::kUnits], vx[2][C::kUnits];  // a pair of tiles on its way
-  auto load = [&](int u, const uint8_t* codes, uint4 (&x)[2][C::kUnits]) {
-    if (2 * u < w.count) wait_or_abort(ms, &ms.at_full[u % kPairBufs], (u / kPairBufs) & 1, a.err);
+  uint4 kx[C::kPer][C::kUnits], vx[C::kPer][C::kUnits];  // a stage on its way
+  auto load = [&](int u, const uint8_t* codes, uint4 (&x)[C::kPer][C::kUnits]) {
+    const int pair = u * C::kPer / 2;
+    if (C::kPer * u < w.count) wait_or_abort(ms, &ms.at_full[pair % kPairBufs], (pair / kPairBufs) & 1, a.err);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (2 * u + j < w.count) load_units<D>(ms.src[(2 * u + j) % (2 * kPairBufs)], codes, un, x[j]);
+    for (int j = 0; j < C::kPer; ++j)
+      if (C::kPer * u + j < w.count)
+        load_units<D>(ms.src[(C::kPer * u + j) % (2 * kPairBufs)], codes, a.cache.dim, un, x[j]);
   };
-  auto store = [&](int u, uint32_t off, uint64_t* full, uint64_t* free, const uint4 (&x)[2][C::kUnits]) {
+  auto store = [&](int u, uint32_t off, uint64_t* full, uint64_t* free, const uint4 (&x)[C::kPer][C::kUnits]) {
     const int st = u % kStages;
     if (u >= kStages) wait_or_abort(ms, &free[st], (u / kStages - 1) & 1, a.err);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = 2 * u + j;
+    for (int j = 0; j < C::kPer; ++j) {
+      const int t = C::kPer * u + j;
       if (t >= w.count) break;
-      const int left = w.n - w.tiles.at(t) * kTile;
-      uint8_t* tile = smem + off + (2 * st + j) * C::kTileBytes;
+      const int left = w.n - w.tile(t) * kTile;
+      uint8_t* tile = smem + off + (C::kPer * st + j) * C::kTileBytes;
       if (left >= kTile) store_units<D, true>(tile, un, x[j], left);
       else store_units<D, false>(tile, un, x[j], left);
     }
@@ -199,7 +207,7 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   };
   load(0, kc, kx);
   load(0, vc, vx);
-  for (int u = 0; 2 * u < w.count; ++u) {
+  for (int u = 0; C::kPer * u < w.count; ++u) {
     store(u, C::kOffK, ms.k_full, ms.k_free, kx);
     load(u + 1, kc, kx);
     store(u, C::kOffV, ms.v_full, ms.v_free, vx);
@@ -210,7 +218,6 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
 // ------------------------------------------------------------------ addresses and scales
 
 // Four pairs of tiles at a time, 16 tokens a lane: where they are, and their scales.
-template <int D>
 __device__ void look_up_role(const Kv8AttnArgs& a, const Part& w, Misc& ms) {
   const int lane = threadIdx.x & 31, g = lane % kGroups, P = a.cache.rows_per_block, shift = 31 - __clz(P);
   float inv_top = 0.f;
@@ -219,12 +226,12 @@ __device__ void look_up_role(const Kv8AttnArgs& a, const Part& w, Misc& ms) {
     float ks = -1.f, vs = 1.f;
     int64_t src = -1;
     if (t < w.count) {
-      const int tok = w.tiles.at(t) * kTile + 16 * g;
+      const int tok = w.tile(t) * kTile + 16 * g;
       if (tok < w.n) {
         const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok >> shift);
         if (blk >= 0) {
           const int64_t at = (int64_t)blk * a.cache.kv_heads + w.kvh;
-          src = (at * P + (tok & (P - 1))) * D;
+          src = (at * P + (tok & (P - 1))) * a.cache.dim;
           ks = a.cache.k_scale[at];
           vs = a.cache.v_scale[at];
         } else {
@@ -249,7 +256,7 @@ __device__ void look_up_role(const Kv8AttnArgs& a, const Part& w, Misc& ms) {
     // of the four lanes of a tile: all of its tokens are there, and no row's mask cuts it
     const uint32_t there = __ballot_sync(0xffffffffu, src >= 0);
     if (t < w.count && g == 0) {
-      const int t0 = w.tiles.at(t) * kTile;
+      const int t0 = w.tile(t) * kTile;
       ms.plain[sb] = (there >> lane & 15u) == 15u && t0 + kTile <= w.n && t0 >= w.all_first &&
                      ((t0 >= w.all_lo && t0 + kTile - 1 <= w.all_p) || t0 + kTile <= w.pre);
     }
@@ -276,12 +283,12 @@ __device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, const Part& w, ui
   const bool lead = elect_one();
   bool ok = wait_or_abort(ms, &ms.q_full, 0, a.err);
   auto products_s = [&](int t) {  // S_0(t), S_1(t)
-    const int st = (t >> 1) % kStages;
-    if (!(t & 1)) ok = ok && wait_or_abort(ms, &ms.k_full[st], (t >> 1) / kStages & 1, a.err);
-    const uint32_t ko = (t % (2 * kStages) * C::kTileBytes) >> 4;
+    const int st = t / C::kPer % kStages;
+    if (t % C::kPer == 0) ok = ok && wait_or_abort(ms, &ms.k_full[st], t / C::kPer / kStages & 1, a.err);
+    const uint32_t ko = (t % (C::kPer * kStages) * C::kTileBytes) >> 4;
     if (lead) {
 #pragma unroll
-      for (int i = 0; i < kMTiles; ++i) {
+      for (int i = 0; i < C::kMT; ++i) {
         if (ok) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
@@ -291,18 +298,18 @@ __device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, const Part& w, ui
         }
         mma_commit(&ms.s_full[i][t & 1]);
       }
-      if (t & 1) mma_commit(&ms.k_free[st]);
+      if (t % C::kPer == C::kPer - 1) mma_commit(&ms.k_free[st]);
     }
     __syncwarp();
   };
   if (n > 0) products_s(0);
   for (int t = 0; t < n; ++t) {
     if (t + 1 < n) products_s(t + 1);  // over P_i(t - 1), which O_i(t - 1) has read
-    const int st = (t >> 1) % kStages;
-    if (!(t & 1)) ok = ok && wait_or_abort(ms, &ms.v_full[st], (t >> 1) / kStages & 1, a.err);
-    const uint32_t vo = (t % (2 * kStages) * C::kTileBytes) >> 4;
+    const int st = t / C::kPer % kStages;
+    if (t % C::kPer == 0) ok = ok && wait_or_abort(ms, &ms.v_full[st], t / C::kPer / kStages & 1, a.err);
+    const uint32_t vo = (t % (C::kPer * kStages) * C::kTileBytes) >> 4;
 #pragma unroll
-    for (int i = 0; i < kMTiles; ++i) {
+    for (int i = 0; i < C::kMT; ++i) {
       ok = ok && wait_or_abort(ms, &ms.p_full[i][t & 1], (t >> 1) & 1, a.err);
       tc_fence_after();
       if (lead) {
@@ -313,7 +320,7 @@ __device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, const Part& w, ui
                        idesc_o, (t | ks) != 0);
         }
         mma_commit(&ms.o_done[i][t & 1]);
-        if (i == kMTiles - 1 && (t & 1)) mma_commit(&ms.v_free[st]);
+        if (i == C::kMT - 1 && t % C::kPer == C::kPer - 1) mma_commit(&ms.v_free[st]);
       }
       __syncwarp();
     }
@@ -326,6 +333,12 @@ __device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, const Part& w, ui
 
 // ------------------------------------------------------------------ softmax
 
+// First row of a CTA's partial results.
+template <int D>
+__device__ __forceinline__ int64_t part_slot(int64_t gx, int64_t x, int kvh, int split, int n_splits) {
+  return ((kvh * gx + x) * n_splits + split) * (Cfg<D>::kMT * kM);
+}
+
 // Bits [a, b) of 64, whatever a and b are.
 __device__ __forceinline__ uint64_t key_bits(int64_t a, int64_t b) {
   a = max((int64_t)0, min((int64_t)64, a));
@@ -336,7 +349,8 @@ __device__ __forceinline__ uint64_t key_bits(int64_t a, int64_t b) {
 template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem, int st) {
   using C = Cfg<D>;
-  const int i = st >> 7, m_row = st & 127, G = a.group;
+  const int i = st >> 7, m_row = st & 127, G = a.group, dim = a.cache.dim;
+  if (i >= C::kMT) return;
   const int tok = w.i0 + i * w.tpt + m_row / G, head = w.kvh * G + m_row % G;
   const bool real = m_row < w.tpt * G && tok < w.r.rows();
   const int64_t row = w.r.r0 + tok;
@@ -345,9 +359,9 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
   float p2 = 1.f;
   {
     uint8_t* tile = smem + i * C::kQBytes;
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + row * a.q_stride + (int64_t)head * D;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + row * a.q_stride + (int64_t)head * dim;
     auto piece = [&](int c) {  // 8 dims
-      if (!real) return make_uint4(0, 0, 0, 0);
+      if (!real || 8 * c >= dim) return make_uint4(0, 0, 0, 0);
       if (a.q_vec) return __ldg(reinterpret_cast<const uint4*>(q) + c);
       uint32_t e[4];
 #pragma unroll
@@ -390,7 +404,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
   float m = -FLT_MAX, l = 0.f;
 
   for (int t = 0; t < w.count; ++t) {
-    const int u = t >> 1, sb = t % (2 * kPairBufs), t0 = w.tiles.at(t) * kTile;
+    const int u = t >> 1, sb = t % (2 * kPairBufs), t0 = w.tile(t) * kTile;
     const uint32_t s_addr = lane_addr + kTile * (2 * i + (t & 1));
     wait_or_abort(ms, &ms.at_full[u % kPairBufs], (u / kPairBufs) & 1, a.err);
     // what turns the accumulator's 16 columns into scores in log2 units, before the cap; not 0, so
@@ -413,6 +427,20 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
         x[k] = y - slope * fabsf((float)(p - t0) - (float)k);
       }
     }
+    // scores of at most the cap in magnitude, before it, hidden ones too
+    bool small = CAP && !BIAS;
+    if constexpr (CAP && !BIAS) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float* y = x + 16 * g;
+        float z[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          z[k] = fmaxf(fmaxf(fabsf(y[k]), fabsf(y[k + 4])), fmaxf(fabsf(y[k + 8]), fabsf(y[k + 12])));
+        small &= fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) * f[g] <= 2.0f * kLog2e;
+      }
+      small = __all_sync(0xffffffffu, small);
+    }
     uint64_t see = ~0ull;  // a bit for each key that the row sees
     if (!plain) {
       see = key_bits(lo - t0, (int64_t)p + 1 - t0) | key_bits(first - t0, w.pre - t0);
@@ -426,7 +454,6 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     // the cap rises with the accumulator: without a bias only the maximum is capped here (one over
     // hidden keys alone gives -cap, at or below every score)
     float mt = -INFINITY;
-    bool small = CAP && !BIAS;  // scores of at most the cap in magnitude, before it
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float* y = x + 16 * g;
@@ -435,14 +462,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
       for (int k = 0; k < 4; ++k) z[k] = fmaxf(fmaxf(y[k], y[k + 4]), fmaxf(y[k + 8], y[k + 12]));
       const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
       mt = fmaxf(mt, BIAS ? top : CAP ? post * tanh_exp2(top * f[g]) : top * f[g]);
-      if constexpr (CAP && !BIAS) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) z[k] = fminf(fminf(y[k], y[k + 4]), fminf(y[k + 8], y[k + 12]));
-        const float low = fminf(fminf(z[0], z[1]), fminf(z[2], z[3]));
-        small &= fmaxf(top, -low) * f[g] <= 2.0f * kLog2e;
-      }
     }
-    small = CAP && !BIAS && __all_sync(0xffffffffu, small);
     if (__any_sync(0xffffffffu, mt > m + kRescaleMargin)) {
       const float mn = fmaxf(m, mt), alpha = fast_exp2(m - mn);
       m = mn;
@@ -491,7 +511,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
             e = fma2(e, make_float2(f[g], f[g]), make_float2(add, add));
           }
           e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-          if constexpr (kHow == 1) {  // -inf does not pass the cap
+          if constexpr (kHow != 0) {  // -inf does not pass the cap
             if (!plain) {
               e.x = see >> (16 * g + 2 * k) & 1 ? e.x : 0.f;
               e.y = see >> (16 * g + 2 * k + 1) & 1 ? e.y : 0.f;
@@ -522,8 +542,10 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
   // ---- result
   if (w.count > 0) wait_or_abort(ms, &ms.o_done[i][(w.count - 1) & 1], ((w.count - 1) >> 1) & 1, a.err);
   tc_fence_after();
-  const float inv = l == 0.f ? 0.f : ms.v_max / l;
-  uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (row * a.heads + head) * D;
+  const bool part = a.n_splits > 1;  // one of several shares of the keys: O and l as they are
+  const float inv = part ? ms.v_max : l == 0.f ? 0.f : ms.v_max / l;
+  const int64_t slot = part_slot<D>(gridDim.x, w.x, w.kvh, blockIdx.z, a.n_splits) + st;
+  uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (row * a.heads + head) * dim;
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     float o[16];
@@ -531,7 +553,16 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
       tmem_ld16(o_addr + 16 * c, o);
       tmem_wait_ld();
     }
-    if (!real) continue;
+    if (!real || 16 * c >= dim) continue;
+    if (part) {
+      float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + 16 * c);
+      if (l != 0.f) {  // else it is not read
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+      }
+      continue;
+    }
     uint32_t z[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) z[k] = w.count > 0 ? f32x2_to_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
@@ -543,8 +574,36 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
       for (int k = 0; k < 8; ++k) out[16 * c + 2 * k] = (uint16_t)z[k], out[16 * c + 2 * k + 1] = (uint16_t)(z[k] >> 16);
     }
   }
-  if (real && a.lse) a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
+  if (real && part) {
+    a.part_ml[2 * slot] = m;
+    a.part_ml[2 * slot + 1] = l;
+  } else if (real && a.lse) {
+    a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
+  }
   tc_fence_before();
+}
+
+// The part of the grid's x for key head blockIdx.y: with T tokens a CTA and f(b) = row_start[b] / T + b,
+// request b owns the x in [f(b), f(b + 1)), at least rows / T + 1 of them.  False: no rows there, or
+// the few-row kernel's.  Called by whole warps, after which `owner` needs a barrier.
+template <int D>
+__device__ __forceinline__ bool find_part(const Kv8AttnArgs& a, int64_t x, int32_t& owner, Part& w) {
+  w.tpt = kM / a.group;
+  const int T = Cfg<D>::kMT * w.tpt;
+  auto first_x = [&](int b) { return (int64_t)a.row_start[b] / T + b; };
+  if (threadIdx.x < 32) {
+    const int b = warp_last_le(a.bt.num_seqs, x, first_x);
+    if (threadIdx.x == 0) owner = b;
+  }
+  __syncthreads();
+  w.b = owner;
+  w.kvh = blockIdx.y;
+  w.x = (int32_t)x;
+  if (!kv8_request(a.row_start, a.cached, w.b, a.n_rows, a.bt, a.cache.rows_per_block, w.r, a.err)) return false;
+  const int n_new = w.r.rows();
+  if ((int64_t)n_new * a.group <= a.few_cols || n_new > a.max_new || x < first_x(w.b)) return false;
+  w.i0 = (int)min((x - first_x(w.b)) * T, (int64_t)n_new);
+  return w.i0 < n_new;
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -561,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
       mbar_init(&ms.k_free[s], 1);
       mbar_init(&ms.v_free[s], 1);
     }
-    for (int i = 0; i < kMTiles; ++i) {
+    for (int i = 0; i < C::kMT; ++i) {
       for (int s = 0; s < 2; ++s) {
         mbar_init(&ms.s_full[i][s], 1);
         mbar_init(&ms.p_full[i][s], 128);
@@ -570,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
     }
     for (int u = 0; u < kPairBufs; ++u) {
       mbar_init(&ms.at_full[u], 1);
-      mbar_init(&ms.at_free[u], kSoftmax / 32);
+      mbar_init(&ms.at_free[u], C::kMT * 4);
     }
-    mbar_init(&ms.q_full, kSoftmax);
+    mbar_init(&ms.q_full, C::kMT * 128);
     mbar_init(&ms.mma_done, 1);
     ms.abort = 0;
     ms.v_max = 1.f;
@@ -581,41 +640,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
   pdl_trigger();
   pdl_wait();
 
-  // ---- the CTA's part: with T tokens a CTA and f(b) = row_start[b] / T + b, request b owns the x in
-  // [f(b), f(b + 1)), at least rows / T + 1 of them.  Later parts see more keys and go first.
+  // ---- the CTA's part; later parts see more keys and go first
   Part w{};
-  w.tpt = kM / a.group;
-  const int T = kMTiles * w.tpt;
-  const int64_t x = gridDim.x - 1 - blockIdx.x;
-  auto first_x = [&](int b) { return (int64_t)a.row_start[b] / T + b; };
-  if (wid == 0) {
-    const int b = warp_last_le(a.bt.num_seqs, x, first_x);
-    if (tid == 0) ms.owner = b;
-  }
-  __syncthreads();
-  w.b = ms.owner;
-  w.kvh = blockIdx.y;
-  if (!kv8_request(a.row_start, a.cached, w.b, a.n_rows, a.bt, a.cache.rows_per_block, w.r, a.err)) return;
-  const int n_new = w.r.rows();
-  if ((int64_t)n_new * a.group <= a.few_cols || n_new > a.max_new || x < first_x(w.b)) return;  // the few-row kernel's
-  w.i0 = (int)min((x - first_x(w.b)) * T, (int64_t)n_new);
-  if (w.i0 >= n_new) return;
+  if (!find_part<D>(a, gridDim.x - 1 - blockIdx.x, ms.owner, w)) return;
+  const int n_new = w.r.rows(), T = C::kMT * w.tpt;
   const int last = min(n_new, w.i0 + T) - 1;  // token
   w.n = w.r.len();
   w.pre = a.mask.prefix ? min(a.mask.prefix[w.b], w.n) : 0;
   if (a.mask.first) {
-    w.first = INT32_MAX;
-    for (int i = w.i0; i <= last; ++i) {
+    int32_t low = INT32_MAX, high = 0;
+    for (int i = w.i0 + (tid & 31); i <= last; i += 32) {
       const int32_t f = max(a.mask.first[w.r.r0 + i], 0);
-      w.first = min(w.first, f);
-      w.all_first = max(w.all_first, f);
+      low = min(low, f);
+      high = max(high, f);
     }
+    w.first = __reduce_min_sync(0xffffffffu, low);
+    w.all_first = __reduce_max_sync(0xffffffffu, high);
   }
   w.all_p = w.r.cached + w.i0;
   w.all_lo = a.mask.window > 0 ? max(w.all_first, w.r.cached + last - a.mask.window + 1) : w.all_first;
   const int lo = a.mask.window > 0 ? max(w.first, w.r.cached + w.i0 - a.mask.window + 1) : w.first;
   w.tiles = kv8_tiles(kTile, w.first, w.pre, lo, w.r.cached + last);
-  w.count = w.tiles.count();
+  const int64_t all = w.tiles.count();
+  w.begin = (int32_t)(all * blockIdx.z / a.n_splits);
+  w.count = (int32_t)(all * (blockIdx.z + 1) / a.n_splits) - w.begin;
 
   if (wid == kMmaWarp) tmem_alloc(&ms.tmem_base, 512);
   tc_fence_before();
@@ -626,12 +674,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
     softmax_role<D, CAP, BIAS>(a, w, smem, ms, tmem, tid);
   } else {
     if (wid < kMmaWarp) convert_role<D>(a, w, smem, ms, tid - kSoftmax);
-    else if (wid == kLookWarp) look_up_role<D>(a, w, ms);
+    else if (wid == kLookWarp) look_up_role(a, w, ms);
     else mma_role<D>(a, w, smem, ms, tmem);
   }
   __syncthreads();
   tc_fence_after();
   if (wid == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the shares of the keys, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) kv8_prefill_join_kernel(const Kv8AttnArgs a) {
+  __shared__ int32_t owner;
+  pdl_trigger();
+  pdl_wait();
+  Part w{};
+  if (!find_part<D>(a, blockIdx.x, owner, w)) return;
+  const int lane = threadIdx.x & 31, G = a.group, dim = a.cache.dim, S = a.n_splits;
+  const int st = blockIdx.z * 4 + (threadIdx.x >> 5), m_row = st & (kM - 1);
+  const int tok = w.i0 + (st / kM) * w.tpt + m_row / G, head = w.kvh * G + m_row % G;
+  if (m_row >= w.tpt * G || tok >= w.r.rows()) return;
+  auto slot = [&](int s) { return part_slot<D>(gridDim.x, w.x, w.kvh, s, S) + st; };
+  float m = -FLT_MAX;
+  for (int s = 0; s < S; ++s) m = fmaxf(m, a.part_ml[2 * slot(s)]);
+  float l = 0.f, o[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
+  for (int s = 0; s < S; ++s) {
+    const float ls = a.part_ml[2 * slot(s) + 1], f = fast_exp2(a.part_ml[2 * slot(s)] - m);
+    if (ls == 0.f) continue;  // saw nothing
+    l += ls * f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+      if (lane + 32 * k < dim) o[k] += a.part_o[slot(s) * D + lane + 32 * k] * f;
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int64_t rh = (int64_t)(w.r.r0 + tok) * a.heads + head;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k)
+    if (lane + 32 * k < dim) reinterpret_cast<uint16_t*>(a.out)[rh * dim + lane + 32 * k] = f32_to_bf16(o[k] * inv);
+  if (a.lse && lane == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
+}
+
+// The head size of the kernel that takes `dim`.
+int32_t tile_dim(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+int64_t grid_x(int32_t n_rows, int32_t num_seqs, int32_t group, int32_t dim) {
+  const int32_t tiles = tile_dim(dim) == 256 ? Cfg<256>::kMT : Cfg<128>::kMT;
+  return (int64_t)n_rows / (tiles * (kM / group)) + num_seqs;
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -645,9 +735,11 @@ cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t s) {
     return err;
   });
   if (e != cudaSuccess) return e;
-  const unsigned gx = (unsigned)(a.n_rows / (kMTiles * (kM / a.group)) + a.bt.num_seqs);
-  return launch_k(kv8_prefill_kernel<D, CAP, BIAS>, dim3(gx, a.cache.kv_heads), dim3(kThreads), smem_bytes<D>(), s, 0,
-                  a);
+  const unsigned gx = (unsigned)grid_x(a.n_rows, a.bt.num_seqs, a.group, D), hk = (unsigned)a.cache.kv_heads;
+  const cudaError_t k = launch_k(kv8_prefill_kernel<D, CAP, BIAS>, dim3(gx, hk, a.n_splits), dim3(kThreads),
+                                 smem_bytes<D>(), s, 0, a);
+  if (k != cudaSuccess || a.n_splits == 1) return k;
+  return launch_k(kv8_prefill_join_kernel<D>, dim3(gx, hk, Cfg<D>::kMT * kM / 4), dim3(128), 0, s, 0, a);
 }
 
 template <int D>
@@ -657,12 +749,41 @@ cudaError_t launch_dim(const Kv8AttnArgs& a, cudaStream_t s) {
   return bias ? launch<D, false, true>(a, s) : launch<D, false, false>(a, s);
 }
 
+constexpr int kSms = 152;  // of a GB300
+
 }  // namespace
 
-bool kv8_prefill_eligible(int32_t dim, int32_t group) { return (dim == 64 || dim == 128) && group <= kM; }
+bool kv8_prefill_eligible(int32_t group) { return group <= kM; }
+
+// A few parts over long sequences leave most SMs idle, so their keys are shared out: to as many
+// CTAs as one wave holds, each with 8 tiles or more of the `max_len` tokens that the table can
+// map, and 16 at most.  PREFILL_SPLIT
+int32_t kv8_prefill_splits(int32_t n_rows, int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t dim,
+                           int64_t max_len) {
+  const int64_t ctas = grid_x(n_rows, num_seqs, heads / kv_heads, dim) * kv_heads;
+  int64_t s = kSms / ctas;
+  const int64_t most = max_len / (8 * kTile);
+  if (s > most) s = most;
+  return (int32_t)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+
+size_t kv8_prefill_workspace(int32_t n_rows, int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t dim,
+                             int32_t splits) {
+  if (splits <= 1) return 0;
+  const int32_t D = tile_dim(dim), rows = (D == 256 ? Cfg<256>::kMT : Cfg<128>::kMT) * kM;
+  return (size_t)grid_x(n_rows, num_seqs, heads / kv_heads, dim) * kv_heads * splits * rows * (D + 2) * sizeof(float);
+}
+
+void kv8_prefill_parts(Kv8AttnArgs& a, void* ws) {
+  const int32_t D = tile_dim(a.cache.dim), rows = (D == 256 ? Cfg<256>::kMT : Cfg<128>::kMT) * kM;
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = a.part_o + (size_t)grid_x(a.n_rows, a.bt.num_seqs, a.group, a.cache.dim) * a.cache.kv_heads *
+                             a.n_splits * rows * D;
+}
 
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s) {
-  return a.cache.dim == 64 ? launch_dim<64>(a, s) : launch_dim<128>(a, s);
+  const int32_t D = tile_dim(a.cache.dim);
+  return D == 64 ? launch_dim<64>(a, s) : D == 128 ? launch_dim<128>(a, s) : launch_dim<256>(a, s);
 }
 
 }  // namespace csa

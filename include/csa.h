@@ -404,7 +404,7 @@ CSA_API int csa_kv8_store(const void* k, const void* v, int32_t in_dtype, int64_
  */
 typedef struct {
   float scale;           /* > 0 */
-  float softcap;         /* >= 0; 0: none */
+  float softcap;         /* 0: none; else 2^-64 or more */
   int32_t window;        /* >= 0; 0: none */
   const float* slopes;   /* device [heads], or NULL */
   const int32_t* first;  /* device [n_rows], or NULL: 0 */
@@ -425,8 +425,9 @@ typedef struct {
  *   row_start, cached as in csa_kv8_store
  *   ws   at least csa_kv8_attn_workspace_size(...) bytes, 16-byte aligned.  Scratch:
  *        nothing needs to start at zero, and calls that can overlap need their own.
- * Probabilities are rounded to fp16 before they meet the values when q and out are
- * BF16 and dim is 64, 128 or 256; otherwise everything stays in fp32.
+ * With BF16 q and out, probabilities (times their block's value scale) are rounded to
+ * fp16 before they meet the values: 11 bits as long as that product is within 2^-21
+ * of the largest a request's rows meet, fewer below.  Otherwise everything stays in fp32.
  * A request with more than max_new rows, or out of bounds as in csa_kv8_store, is
  * skipped; keys in unmapped blocks are skipped (CSA_ERR_DEVICE_BOUNDS).
  */

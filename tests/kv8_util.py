@@ -75,8 +75,8 @@ class Batch:
         """Compare with the oracle; the tolerance is each rounding's half step.
 
         The scores: fp32 sums of D products, an error of at most (D + 8) 2^-23 of the sum of magnitudes (the
-        tensor cores add with truncation, twice the half step), and 2^-21 of the cap or of the bias from tanh
-        and exp.  A score off by d changes a weight by 2 d of itself.  bf16 outputs may come from weights in
+        tensor cores add with truncation, twice the half step), and 2^-21 of the capped score or of the bias from
+        tanh and exp.  A score off by d changes a weight by 2 d of itself.  bf16 outputs may come from weights in
         fp16 (half a step: 2^-11) and are rounded to bf16 (2^-8); fp32 ones are sums over n keys, n 2^-24."""
         half = out.dtype == torch.bfloat16
         out, lse = out.double().numpy(), None if lse is None else lse.double().numpy()
@@ -95,7 +95,8 @@ class Batch:
                 hs = slice(h * G, (h + 1) * G)
                 want, wl, wabs, mag = K.attend(q[r0:r1, hs], k, v, p, see, scale, softcap,
                                                None if slopes is None else np.asarray(slopes)[hs])
-                d = (self.D + 8) * 2.0 ** -23 * mag + 2.0 ** -21 * (softcap + (mag if slopes is not None else 0) + 1)
+                capped = np.minimum(softcap, mag) if softcap else 0.0
+                d = (self.D + 8) * 2.0 ** -23 * mag + 2.0 ** -21 * (capped + (mag if slopes is not None else 0) + 1)
                 rel = 2 * d + (2.0 ** -11 if half else 0) + n * 2.0 ** -24
                 tol = rel[..., None] * wabs + np.abs(want) * (2.0 ** -8 if half else 2.0 ** -23) + 1e-30
                 got = out[r0:r1, hs]

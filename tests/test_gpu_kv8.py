@@ -200,6 +200,14 @@ SHAPES = [
     ([10], [70], 48, 1, 128, 32, BF),
     ([64], [140], 4, 2, 256, 256, BF),
     ([33, 200], [1, 40], 4, 2, 96, 32, BF),
+    ([500, 40], [1, 2], 4, 2, 16, 16, BF),
+    ([90], [80], 8, 2, 48, 64, BF),
+    ([300, 5], [2, 90], 6, 2, 112, 32, BF),
+    ([200, 77], [1, 60], 10, 2, 160, 64, BF),
+    ([400], [50], 4, 4, 240, 128, BF),
+    ([6000], [37], 16, 2, 128, 256, BF),
+    ([5000, 9], [90, 1], 4, 1, 64, 64, BF),
+    ([4100], [50], 8, 1, 192, 32, BF),
     ([100, 7], [1, 30], 12, 4, 80, 16, F32),
     ([1500], [1], 8, 8, 128, 64, F32),
     ([20], [33], 9, 3, 16, 16, F32),
@@ -248,6 +256,19 @@ def test_attn_types_strides_and_scale():
     out, lse, st = b.attn(q=q)
     assert st == csa.OK
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("softcap", [0.3, 30.0, 1e3, 1e6])
+@pytest.mark.parametrize("new", [2, 150])
+def test_caps_near_and_far_above_the_scores(new, softcap):
+    b = Batch([400, 3], [new, new], 8, 2, 128, 64, BF, seed=13)
+    out, lse, st = b.attn(softcap=softcap)
+    assert st == csa.OK
+    b.check(out, lse, softcap=softcap)
+    c = Batch([60], [7], 4, 2, 80, 32, F32, seed=13)
+    out, lse, st = c.attn(softcap=softcap)
+    assert st == csa.OK
+    c.check(out, lse, softcap=softcap)
 
 
 @pytest.mark.parametrize("factor", [1e-30, 1e4, 1e30])

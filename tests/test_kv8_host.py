@@ -60,7 +60,7 @@ def test_attn_refusals(lib):
     for b in (dict(q=None), dict(out=None), dict(err=None), dict(start=None), dict(cached=None), dict(n=-1), dict(heads=0),
               dict(heads=7), dict(max_new=-1), dict(qs=-1), dict(q=0x101), dict(out=0x102, od=csa.F32), dict(cache=_cache(v=None)),
               *(dict(mask=csa.Kv8MaskC(*m, None, None, None)) for m in
-                ((0.0, 0, 0), (-1.0, 0, 0), (nan, 0, 0), (inf, 0, 0), (1, -1, 0), (1, nan, 0), (1, inf, 0), (1, 0, -1)))):
+                ((0.0, 0, 0), (-1.0, 0, 0), (nan, 0, 0), (inf, 0, 0), (1, -1, 0), (1, 1e-20, 0), (1, nan, 0), (1, inf, 0), (1, 0, -1)))):
         assert call(**b) == csa.ERR_INVALID_ARG, b
     for b in (dict(qd=csa.E4M3), dict(od=csa.E4M3), dict(cache=_cache(dim=40)), dict(heads=70000, cache=_cache(kv_heads=1))):
         assert call(**b) == csa.ERR_UNSUPPORTED, b
