@@ -112,7 +112,9 @@ struct Part {
 template <int D>
 struct Unit {
   int row, piece;  // row: of the thread's first unit, the others kConvert 16 / D further each
-  __device__ __forceinline__ explicit Unit(int ct) {
+  int off, step;   // within 16 tokens' codes; step: of every other unit, when rows are 8 apart
+  bool there;      // the piece is not past the head size
+  __device__ __forceinline__ Unit(int ct, int dim) {
     if constexpr (D == 64) {  // 32 rows of 4 pieces
       row = ct >> 2, piece = ct & 3;
     } else if constexpr (D == 128) {  // 16 rows of 8
@@ -120,18 +122,21 @@ struct Unit {
     } else {  // 8 rows of 16
       row = ((ct >> 2) & 1) + 2 * (ct >> 5), piece = (ct & 3) + ((ct >> 1) & 12);
     }
+    off = row % 16 * dim + piece * 16;
+    step = D == 256 ? 8 * dim : 0;
+    there = piece * 16 < dim;
   }
 };
 
 template <int D>
-__device__ __forceinline__ void load_units(const int64_t* src, const uint8_t* codes, int dim, const Unit<D>& un, uint4* x) {
+__device__ __forceinline__ void load_units(const int64_t* src, const uint8_t* codes, const Unit<D>& un, uint4* x) {
   constexpr int kRows = kConvert / (D / 16);
 #pragma unroll
   for (int i = 0; i < Cfg<D>::kUnits; ++i) {
     const int row = un.row + i * kRows;
-    const int64_t at = un.piece * 16 < dim ? src[row / 16] : -1;  // tokens past the sequence hold any code
-    x[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at + (row % 16) * dim + un.piece * 16))
-                   : make_uint4(0, 0, 0, 0);
+    const int64_t at = src[row / 16];  // tokens past the sequence hold any code
+    x[i] = at >= 0 && un.there ? __ldg(reinterpret_cast<const uint4*>(codes + at + un.off + (i & 1) * un.step))
+                               : make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -180,7 +185,7 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
   for (int i = 0; i < kConvert / 32; ++i) top = fmaxf(top, ms.red[i]);
   if (ct == 0) ms.v_max = top;
   named_bar(2, kConvert + 32);  // for the look-up warp, which passes it on
-  const Unit<D> un(ct);
+  const Unit<D> un(ct, a.cache.dim);
   uint4 kx[C::kPer][C::kUnits], vx[C::kPer][C::kUnits];  // a stage on its way
   auto load = [&](int u, const uint8_t* codes, uint4 (&x)[C::kPer][C::kUnits]) {
     const int pair = u * C::kPer / 2;
@@ -188,7 +193,7 @@ __device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem,
 #pragma unroll
     for (int j = 0; j < C::kPer; ++j)
       if (C::kPer * u + j < w.count)
-        load_units<D>(ms.src[(C::kPer * u + j) % (2 * kPairBufs)], codes, a.cache.dim, un, x[j]);
+        load_units<D>(ms.src[(C::kPer * u + j) % (2 * kPairBufs)], codes, un, x[j]);
   };
   auto store = [&](int u, uint32_t off, uint64_t* full, uint64_t* free, const uint4 (&x)[C::kPer][C::kUnits]) {
     const int st = u % kStages;
@@ -427,23 +432,23 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
         x[k] = y - slope * fabsf((float)(p - t0) - (float)k);
       }
     }
-    // scores of at most the cap in magnitude, before it, hidden ones too
-    bool small = CAP && !BIAS;
-    if constexpr (CAP && !BIAS) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float* y = x + 16 * g;
-        float z[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          z[k] = fmaxf(fmaxf(fabsf(y[k]), fabsf(y[k + 4])), fmaxf(fabsf(y[k + 8]), fabsf(y[k + 12])));
-        small &= fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) * f[g] <= 2.0f * kLog2e;
-      }
-      small = __all_sync(0xffffffffu, small);
-    }
-    uint64_t see = ~0ull;  // a bit for each key that the row sees
     if (!plain) {
-      see = key_bits(lo - t0, (int64_t)p + 1 - t0) | key_bits(first - t0, w.pre - t0);
+      if constexpr (CAP && !BIAS) {  // -inf would not pass the cap: it comes first
+        bool small = true;
+#pragma unroll
+        for (int k = 0; k < kTile; ++k) small &= fabsf(x[k]) * f[k / 16] <= 2.0f * kLog2e;
+        small = __all_sync(0xffffffffu, small);
+#pragma unroll
+        for (int k = 0; k < kTile; k += 2) {
+          float2 y = mul2(make_float2(x[k], x[k + 1]), make_float2(f[k / 16], f[k / 16]));
+          y = small ? tanh_small2(mul2(y, make_float2(0.5f / kLog2e, 0.5f / kLog2e)))
+                    : make_float2(tanh_exp2(y.x), tanh_exp2(y.y));
+          x[k] = post * y.x;
+          x[k + 1] = post * y.y;
+        }
+      }
+      // a bit for each key that the row sees
+      uint64_t see = key_bits(lo - t0, (int64_t)p + 1 - t0) | key_bits(first - t0, w.pre - t0);
       see &= key_bits(first - t0, w.n - t0);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g)
@@ -451,9 +456,9 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
       for (int k = 0; k < kTile; ++k) x[k] = see >> k & 1 ? x[k] : -INFINITY;
     }
-    // the cap rises with the accumulator: without a bias only the maximum is capped here (one over
-    // hidden keys alone gives -cap, at or below every score)
+    // the cap rises with the accumulator: without a bias or a mask only the maximum is capped here
     float mt = -INFINITY;
+    bool small = true;  // scores of at most the cap in magnitude, before it
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float* y = x + 16 * g;
@@ -461,8 +466,15 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[k] = fmaxf(fmaxf(y[k], y[k + 4]), fmaxf(y[k + 8], y[k + 12]));
       const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-      mt = fmaxf(mt, BIAS ? top : CAP ? post * tanh_exp2(top * f[g]) : top * f[g]);
+      mt = fmaxf(mt, BIAS || (CAP && !plain) ? top : CAP ? post * tanh_exp2(top * f[g]) : top * f[g]);
+      if constexpr (CAP && !BIAS) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = fminf(fminf(y[k], y[k + 4]), fminf(y[k + 8], y[k + 12]));
+        const float low = fminf(fminf(z[0], z[1]), fminf(z[2], z[3]));
+        small &= fmaxf(top, -low) * f[g] <= 2.0f * kLog2e;
+      }
     }
+    small = CAP && !BIAS && __all_sync(0xffffffffu, small);
     if (__any_sync(0xffffffffu, mt > m + kRescaleMargin)) {
       const float mn = fmaxf(m, mt), alpha = fast_exp2(m - mn);
       m = mn;
@@ -486,7 +498,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     const float4 lv4 = *reinterpret_cast<const float4*>(ms.lv[sb]), rv4 = *reinterpret_cast<const float4*>(ms.rv[sb]);
     const float lv[kGroups] = {lv4.x, lv4.y, lv4.z, lv4.w}, rv[kGroups] = {rv4.x, rv4.y, rv4.z, rv4.w};
     const float shift = kPShift - m;
-    auto write_p = [&](auto how) {  // 0: scores; 1: scores before the cap; 2: the same, all small
+    auto write_p = [&](auto how) {  // of 0: the accumulator; 1: scores; 2, 3: what the cap is for, 3: all small
       constexpr int kHow = decltype(how)::value;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
@@ -497,12 +509,12 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           float2 e = make_float2(y[2 * k], y[2 * k + 1]);
-          if constexpr (BIAS) {
+          if constexpr (kHow == 1) {
             e = add2(e, make_float2(add, add));
-          } else if constexpr (kHow == 2) {
+          } else if constexpr (kHow == 3) {
             const float fu = f[g] * (0.5f / kLog2e);
             e = fma2(tanh_small2(mul2(e, make_float2(fu, fu))), make_float2(post, post), make_float2(add, add));
-          } else if constexpr (kHow == 1) {  // post tanh + add
+          } else if constexpr (kHow == 2) {  // post tanh + add
             e = make_float2(fast_exp2(e.x * f[g]), fast_exp2(e.y * f[g]));
             e = add2(e, make_float2(1.f, 1.f));
             e = make_float2(fast_rcp(e.x), fast_rcp(e.y));
@@ -511,12 +523,6 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
             e = fma2(e, make_float2(f[g], f[g]), make_float2(add, add));
           }
           e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-          if constexpr (kHow != 0) {  // -inf does not pass the cap
-            if (!plain) {
-              e.x = see >> (16 * g + 2 * k) & 1 ? e.x : 0.f;
-              e.y = see >> (16 * g + 2 * k + 1) & 1 ? e.y : 0.f;
-            }
-          }
           sum = k ? add2(sum, e) : e;
           pw[k] = f32x2_to_f16x2(e.x, e.y);
         }
@@ -524,9 +530,12 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
         tmem_st8(s_addr + 8 * g, pw);
       }
     };
-    if constexpr (CAP && !BIAS) {
-      if (small) write_p(std::integral_constant<int, 2>{});
-      else write_p(std::integral_constant<int, 1>{});
+    if constexpr (BIAS) {
+      write_p(std::integral_constant<int, 1>{});
+    } else if constexpr (CAP) {
+      if (!plain) write_p(std::integral_constant<int, 1>{});
+      else if (small) write_p(std::integral_constant<int, 3>{});
+      else write_p(std::integral_constant<int, 2>{});
     } else {
       write_p(std::integral_constant<int, 0>{});
     }
