@@ -44,6 +44,8 @@ int check_kv8(const csa_kv8* c) {
   return CSA_OK;
 }
 
+constexpr size_t kKv8Head = 256;  // bytes before the partial results in a workspace
+
 // How a call is shared between the two tensor-core kernels: columns (rows x group) of a
 // tile of the few-row kernel, the most columns of a request that it takes, and whether
 // the many-row kernel runs too.
@@ -460,7 +462,7 @@ size_t csa_kv8_attn_workspace_size(int32_t n_rows, int32_t num_seqs, int32_t hea
   if (p.many)
     most = std::max(most, kv8_prefill_workspace(n_rows, num_seqs, heads, kv, dim,
                                                 kv8_prefill_splits(n_rows, num_seqs, heads, kv, dim, INT64_MAX)));
-  return align_up(most);
+  return kKv8Head + align_up(most);
 }
 
 int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_rows, int32_t heads,
@@ -507,12 +509,14 @@ int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_row
     const Kv8Plan p = kv8_plan(a.group, max_new);
     a.cols = p.cols;
     a.few_cols = p.few_cols;
-    kv8_decode_parts(a, ws);
+    a.part_next = reinterpret_cast<int32_t*>(ws);
+    void* parts = reinterpret_cast<uint8_t*>(ws) + kKv8Head;
+    kv8_decode_parts(a, parts);
     if (launch_kv8_decode(a, stream) != cudaSuccess) return CSA_ERR_CUDA;
     if (!p.many) return CSA_OK;
     a.n_splits = kv8_prefill_splits(n_rows, bt->num_seqs, heads, cache->kv_heads, cache->dim,
                                     (int64_t)bt->stride * cache->rows_per_block);
-    kv8_prefill_parts(a, ws);
+    kv8_prefill_parts(a, parts);
     return cuda_status(launch_kv8_prefill(a, stream));
   }
   a.n_splits = kv8_simt_splits(n_rows, heads, cache->kv_heads);

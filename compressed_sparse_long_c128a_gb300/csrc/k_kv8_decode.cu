@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
   const int64_t u_end = min(total, u + share);
   int32_t* head = a.part_head + 8 * blockIdx.x;  // a pair that starts here and ends in a later CTA
   if (tid == 0) head[0] = 0;
+  if (tid == 0 && blockIdx.x == 0) *a.part_next = 0;
   if (u >= u_end) return;
 
   int lo = 0, hi = kThreads;  // the last segment that starts at or before u

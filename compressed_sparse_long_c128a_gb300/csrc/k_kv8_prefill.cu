@@ -25,6 +25,7 @@
 //    CTA's rows see, enters the exponent, P = 2^(s - m + 7 + log2(v / v_max)), and is
 //    divided out of each 16 columns' part of the sum.
 
+#include <algorithm>
 #include <cfloat>
 #include <type_traits>
 
@@ -61,23 +62,36 @@ struct Cfg {
   static constexpr int kUnits = kTile * (D / 16) / kConvert;  // 16-byte pieces of a tile a thread
 };
 
+// What a CTA works on: tokens i0 .. of request b for key head kvh.
+struct Part {
+  Kv8Req r;
+  int32_t b, kvh, x, i0, tpt;  // x: of the grid; tpt: tokens of a query tile
+  int32_t n, first, pre;    // tokens stored, the lowest document start, the prefix
+  int32_t all_first, all_lo, all_p;  // what all rows have in common: see from here on, to here
+  Kv8Tiles tiles;
+  int32_t begin, count;     // of the key tiles: this part's share
+  int32_t split;
+  float v_max;              // the largest value scale of its blocks
+  int32_t end;              // no part: there are no more
+  __device__ __forceinline__ int32_t tile(int32_t t) const { return tiles.at(begin + t); }
+};
+
 struct Misc {
   uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
-  // by the parity of t: who waits for a tile may be one tile behind, never two
+  // by the parity of t within its part: who waits for a tile may be one tile behind, never two
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
-  uint64_t at_full[kPairBufs], at_free[kPairBufs], q_full, mma_done;
+  uint64_t at_full[kPairBufs], at_free[kPairBufs], part_full[2], part_free[2], o_free[2], q_full, mma_done;
   uint32_t tmem_base;
   int32_t abort;
-  int32_t owner;
-  float red[kConvert / 32];
-  float v_max;
+  Part part[2];
   // of the last tiles, by 16 tokens: offset of the codes (-1: none), key scale (negative: no block),
-  // log2 of the value scale relative to v_max, and its inverse
+  // log2 of the value scale relative to the part's largest, and its inverse
   int64_t src[2 * kPairBufs][kGroups];
   alignas(16) float ks[2 * kPairBufs][kGroups];
   alignas(16) float lv[2 * kPairBufs][kGroups];
   alignas(16) float rv[2 * kPairBufs][kGroups];
-  int32_t plain[2 * kPairBufs];  // every row of the CTA sees every key of the tile
+  int32_t t0[2 * kPairBufs];     // first token
+  int32_t plain[2 * kPairBufs];  // every row of the part sees every key of the tile
 };
 
 template <int D>
@@ -94,16 +108,26 @@ __device__ __forceinline__ bool wait_or_abort(Misc& ms, uint64_t* bar, uint32_t 
   return false;
 }
 
-// What a CTA works on: tokens [i0, i0 + nt) of request b for key head kvh.
-struct Part {
-  Kv8Req r;
-  int32_t b, kvh, x, i0, tpt;  // x: of the grid; tpt: tokens of a query tile
-  int32_t n, first, pre;    // tokens stored, the lowest document start, the prefix
-  int32_t all_first, all_lo, all_p;  // what all rows have in common: see from here on, to here
-  Kv8Tiles tiles;
-  int32_t begin, count;     // of the key tiles: this CTA's share
-  __device__ __forceinline__ int32_t tile(int32_t t) const { return tiles.at(begin + t); }
+// Where a role stands after the parts it has been through: what the barriers' phases follow.
+struct Past {
+  uint32_t parts = 0, pairs = 0, tiles = 0, even = 0, odd = 0;
+  __device__ __forceinline__ void add(int32_t count) {
+    ++parts;
+    pairs += (count + 1) / 2;
+    tiles += count;
+    even += (count + 1) / 2;
+    odd += count / 2;
+  }
+  // of the buffers by parity: the uses before tile t's
+  __device__ __forceinline__ uint32_t uses(int32_t t) const { return (t & 1 ? odd : even) + (t >> 1); }
 };
+
+// The next part, or null: there is none, or a wait gave up.
+__device__ __forceinline__ const Part* next_part(Misc& ms, const Past& past, int32_t* err) {
+  const uint32_t slot = past.parts & 1;
+  if (!wait_or_abort(ms, &ms.part_full[slot], past.parts >> 1 & 1, err)) return nullptr;
+  return ms.part[slot].end ? nullptr : &ms.part[slot];
+}
 
 // ------------------------------------------------------------------ conversion
 
@@ -160,123 +184,66 @@ __device__ __forceinline__ void store_units(uint8_t* tile, const Unit<D>& un, co
 }
 
 template <int D>
-__device__ void convert_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, int ct) {
+__device__ __forceinline__ void convert_role(const Kv8AttnArgs& a, uint8_t* smem, Misc& ms, int ct) {
   using C = Cfg<D>;
   const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.cache.k);
   const uint8_t* vc = reinterpret_cast<const uint8_t*>(a.cache.v);
-  const int P = a.cache.rows_per_block, Hk = a.cache.kv_heads, shift = 31 - __clz(P);
-  // the largest value scale of the blocks that the tiles touch
-  float top = kKv8MinScale;
-  for (int part = 0; part < 2; ++part) {
-    const int i0 = part ? max(w.begin, w.tiles.nA) : w.begin;
-    const int nt = (part ? w.begin + w.count : min(w.begin + w.count, w.tiles.nA)) - i0, t0 = w.tiles.at(i0) * kTile;
-    const int lb1 = (min(w.n, t0 + nt * kTile) + P - 1) >> shift;
-    if (nt > 0)
-#pragma unroll 4
-      for (int lb = (t0 >> shift) + ct; lb < lb1; lb += kConvert) {
-        const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, lb);
-        if (blk >= 0) top = fmaxf(top, a.cache.v_scale[(int64_t)blk * Hk + w.kvh]);
-      }
-  }
-  top = warp_max(top);
-  if ((ct & 31) == 0) ms.red[ct >> 5] = top;
-  named_bar(1, kConvert);
-#pragma unroll
-  for (int i = 0; i < kConvert / 32; ++i) top = fmaxf(top, ms.red[i]);
-  if (ct == 0) ms.v_max = top;
-  named_bar(2, kConvert + 32);  // for the look-up warp, which passes it on
   const Unit<D> un(ct, a.cache.dim);
-  uint4 kx[C::kPer][C::kUnits], vx[C::kPer][C::kUnits];  // a stage on its way
-  auto load = [&](int u, const uint8_t* codes, uint4 (&x)[C::kPer][C::kUnits]) {
-    const int pair = u * C::kPer / 2;
-    if (C::kPer * u < w.count) wait_or_abort(ms, &ms.at_full[pair % kPairBufs], (pair / kPairBufs) & 1, a.err);
+  Past past;
+  while (const Part* next = next_part(ms, past, a.err)) {
+    const Part& w = *next;
+    const int count = w.count, n = w.n;
+    uint4 kx[C::kPer][C::kUnits], vx[C::kPer][C::kUnits];  // a stage on its way
+    const uint32_t stage0 = C::kPer == 2 ? past.pairs : past.tiles;
+    auto load = [&](int u, const uint8_t* codes, uint4 (&x)[C::kPer][C::kUnits]) {
+      const uint32_t pair = past.pairs + u * C::kPer / 2;
+      if (C::kPer * u < count) wait_or_abort(ms, &ms.at_full[pair % kPairBufs], (pair / kPairBufs) & 1, a.err);
 #pragma unroll
-    for (int j = 0; j < C::kPer; ++j)
-      if (C::kPer * u + j < w.count)
-        load_units<D>(ms.src[(C::kPer * u + j) % (2 * kPairBufs)], codes, un, x[j]);
-  };
-  auto store = [&](int u, uint32_t off, uint64_t* full, uint64_t* free, const uint4 (&x)[C::kPer][C::kUnits]) {
-    const int st = u % kStages;
-    if (u >= kStages) wait_or_abort(ms, &free[st], (u / kStages - 1) & 1, a.err);
-#pragma unroll
-    for (int j = 0; j < C::kPer; ++j) {
-      const int t = C::kPer * u + j;
-      if (t >= w.count) break;
-      const int left = w.n - w.tile(t) * kTile;
-      uint8_t* tile = smem + off + (C::kPer * st + j) * C::kTileBytes;
-      if (left >= kTile) store_units<D, true>(tile, un, x[j], left);
-      else store_units<D, false>(tile, un, x[j], left);
-    }
-    fence_proxy_async();
-    mbar_arrive(&full[st]);
-  };
-  load(0, kc, kx);
-  load(0, vc, vx);
-  for (int u = 0; C::kPer * u < w.count; ++u) {
-    store(u, C::kOffK, ms.k_full, ms.k_free, kx);
-    load(u + 1, kc, kx);
-    store(u, C::kOffV, ms.v_full, ms.v_free, vx);
-    load(u + 1, vc, vx);
-  }
-}
-
-// ------------------------------------------------------------------ addresses and scales
-
-// Four pairs of tiles at a time, 16 tokens a lane: where they are, and their scales.
-__device__ void look_up_role(const Kv8AttnArgs& a, const Part& w, Misc& ms) {
-  const int lane = threadIdx.x & 31, g = lane % kGroups, P = a.cache.rows_per_block, shift = 31 - __clz(P);
-  float inv_top = 0.f;
-  for (int u0 = 0; 2 * u0 < w.count; u0 += 4) {
-    const int t = 2 * u0 + lane / kGroups, sb = t % (2 * kPairBufs);
-    float ks = -1.f, vs = 1.f;
-    int64_t src = -1;
-    if (t < w.count) {
-      const int tok = w.tile(t) * kTile + 16 * g;
-      if (tok < w.n) {
-        const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok >> shift);
-        if (blk >= 0) {
-          const int64_t at = (int64_t)blk * a.cache.kv_heads + w.kvh;
-          src = (at * P + (tok & (P - 1))) * a.cache.dim;
-          ks = a.cache.k_scale[at];
-          vs = a.cache.v_scale[at];
-        } else {
-          record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
-        }
+      for (int j = 0; j < C::kPer; ++j) {
+        const int t = C::kPer * u + j;
+        if (t < count) load_units<D>(ms.src[2 * (pair % kPairBufs) + (t & 1)], codes, un, x[j]);
       }
-    }
-    if (u0 == 0) {
-      named_bar(2, kConvert + 32);
-      inv_top = 1.0f / ms.v_max;
-    } else if (u0 >= kPairBufs) {
-      for (int u = u0; u < u0 + 4 && 2 * u < w.count; ++u)
-        wait_or_abort(ms, &ms.at_free[u % kPairBufs], (u / kPairBufs - 1) & 1, a.err);
-    }
-    if (t < w.count) {
-      if (src >= 0) vs = fmaxf(vs * inv_top, kKv8MinScale);
-      ms.src[sb][g] = src;
-      ms.ks[sb][g] = ks;
-      ms.lv[sb][g] = log2f(vs);
-      ms.rv[sb][g] = 1.0f / vs;
-    }
-    // of the four lanes of a tile: all of its tokens are there, and no row's mask cuts it
-    const uint32_t there = __ballot_sync(0xffffffffu, src >= 0);
-    if (t < w.count && g == 0) {
-      const int t0 = w.tile(t) * kTile;
-      ms.plain[sb] = (there >> lane & 15u) == 15u && t0 + kTile <= w.n && t0 >= w.all_first &&
-                     ((t0 >= w.all_lo && t0 + kTile - 1 <= w.all_p) || t0 + kTile <= w.pre);
+    };
+    auto store = [&](int u, uint32_t off, uint64_t* full, uint64_t* free, const int (&left)[C::kPer],
+                     const uint4 (&x)[C::kPer][C::kUnits]) {
+      const uint32_t at = stage0 + u, st = at % kStages;
+      if (at >= kStages) wait_or_abort(ms, &free[st], (at / kStages - 1) & 1, a.err);
+#pragma unroll
+      for (int j = 0; j < C::kPer; ++j) {
+        const int t = C::kPer * u + j;
+        if (t >= count) break;
+        uint8_t* tile = smem + off + (C::kPer * st + j) * C::kTileBytes;
+        if (left[j] >= kTile) store_units<D, true>(tile, un, x[j], kTile);
+        else store_units<D, false>(tile, un, x[j], left[j]);
+      }
+      fence_proxy_async();
+      mbar_arrive(&full[st]);
+    };
+    load(0, kc, kx);
+    load(0, vc, vx);
+    for (int u = 0; C::kPer * u < count; ++u) {
+      int left[C::kPer];  // tokens from each tile on; kept for V, by whose turn the softmax may have let go of the tile
+#pragma unroll
+      for (int j = 0; j < C::kPer; ++j) {
+        const int t = C::kPer * u + j;
+        left[j] = t < count ? n - ms.t0[2 * ((past.pairs + (t >> 1)) % kPairBufs) + (t & 1)] : 0;
+      }
+      store(u, C::kOffK, ms.k_full, ms.k_free, left, kx);
+      load(u + 1, kc, kx);
+      store(u, C::kOffV, ms.v_full, ms.v_free, left, vx);
+      load(u + 1, vc, vx);
     }
     __syncwarp();
-    if (lane == 0)
-      for (int u = u0; u < u0 + 4 && 2 * u < w.count; ++u) mbar_arrive(&ms.at_full[u % kPairBufs]);
+    if ((ct & 31) == 0) mbar_arrive(&ms.part_free[past.parts & 1]);
+    past.add(count);
   }
-  if (w.count == 0) named_bar(2, kConvert + 32);
 }
 
 // ------------------------------------------------------------------ products
 
 // The whole warp runs this, so that descriptors stay in uniform registers; one lane issues.
 template <int D>
-__device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem_v) {
+__device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, uint8_t* smem, Misc& ms, uint32_t tmem_v) {
   using C = Cfg<D>;
   constexpr uint32_t idesc_s = idesc_f16(kM, kTile, 0, 0);  // Q and K, both K-major
   constexpr uint32_t idesc_o = idesc_f16(kM, D, 0, 1);      // P from TMEM, V [token][dim] MN-major
@@ -284,51 +251,62 @@ __device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, const Part& w, ui
   const uint64_t d_q = sdesc_sw128(base, 16, 1024);
   const uint64_t d_k = sdesc_sw128(base + C::kOffK, 16, 1024);
   const uint64_t d_v = sdesc_sw128(base + C::kOffV, C::kAtom, 1024);
-  const int n = uniform(w.count);
   const bool lead = elect_one();
-  bool ok = wait_or_abort(ms, &ms.q_full, 0, a.err);
-  auto products_s = [&](int t) {  // S_0(t), S_1(t)
-    const int st = t / C::kPer % kStages;
-    if (t % C::kPer == 0) ok = ok && wait_or_abort(ms, &ms.k_full[st], t / C::kPer / kStages & 1, a.err);
-    const uint32_t ko = (t % (C::kPer * kStages) * C::kTileBytes) >> 4;
-    if (lead) {
-#pragma unroll
-      for (int i = 0; i < C::kMT; ++i) {
-        if (ok) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            mma_bf16(tmem + kTile * (2 * i + (t & 1)),
-                     d_q + ((i * C::kQBytes + (ks >> 2) * C::kQAtom + (ks & 3) * 32) >> 4),
-                     d_k + ko + (((ks >> 2) * C::kAtom + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
-        }
-        mma_commit(&ms.s_full[i][t & 1]);
-      }
-      if (t % C::kPer == C::kPer - 1) mma_commit(&ms.k_free[st]);
-    }
-    __syncwarp();
-  };
-  if (n > 0) products_s(0);
-  for (int t = 0; t < n; ++t) {
-    if (t + 1 < n) products_s(t + 1);  // over P_i(t - 1), which O_i(t - 1) has read
-    const int st = t / C::kPer % kStages;
-    if (t % C::kPer == 0) ok = ok && wait_or_abort(ms, &ms.v_full[st], t / C::kPer / kStages & 1, a.err);
-    const uint32_t vo = (t % (C::kPer * kStages) * C::kTileBytes) >> 4;
-#pragma unroll
-    for (int i = 0; i < C::kMT; ++i) {
-      ok = ok && wait_or_abort(ms, &ms.p_full[i][t & 1], (t >> 1) & 1, a.err);
-      tc_fence_after();
+  Past past;
+  while (const Part* next = next_part(ms, past, a.err)) {
+    const Part& w = *next;
+    const int n = uniform(w.count);
+    const uint32_t stage0 = uniform(C::kPer == 2 ? past.pairs : past.tiles);
+    bool ok = wait_or_abort(ms, &ms.q_full, past.parts & 1, a.err);
+    auto products_s = [&](int t) {  // S_0(t), S_1(t)
+      const uint32_t at = stage0 + t / C::kPer, st = at % kStages;
+      if (t % C::kPer == 0) ok = ok && wait_or_abort(ms, &ms.k_full[st], at / kStages & 1, a.err);
+      const uint32_t ko = ((C::kPer * st + t % C::kPer) * C::kTileBytes) >> 4;
       if (lead) {
-        if (ok) {
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_f16_ts(tmem + C::kColO + D * i, tmem + kTile * (2 * i + (t & 1)) + 8 * ks, d_v + vo + ((ks * 2048) >> 4),
-                       idesc_o, (t | ks) != 0);
+        for (int i = 0; i < C::kMT; ++i) {
+          if (ok) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              mma_bf16(tmem + kTile * (2 * i + (t & 1)),
+                       d_q + ((i * C::kQBytes + (ks >> 2) * C::kQAtom + (ks & 3) * 32) >> 4),
+                       d_k + ko + (((ks >> 2) * C::kAtom + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+          }
+          mma_commit(&ms.s_full[i][t & 1]);
         }
-        mma_commit(&ms.o_done[i][t & 1]);
-        if (i == C::kMT - 1 && t % C::kPer == C::kPer - 1) mma_commit(&ms.v_free[st]);
+        if (t % C::kPer == C::kPer - 1 || t == n - 1) mma_commit(&ms.k_free[st]);
       }
       __syncwarp();
+    };
+    if (n > 0) products_s(0);
+    // the last part's O has been read
+    if (past.parts > 0)
+      for (int i = 0; i < C::kMT; ++i) ok = ok && wait_or_abort(ms, &ms.o_free[i], (past.parts - 1) & 1, a.err);
+    for (int t = 0; t < n; ++t) {
+      if (t + 1 < n) products_s(t + 1);  // over P_i(t - 1), which O_i(t - 1) has read
+      const uint32_t at = stage0 + t / C::kPer, st = at % kStages;
+      if (t % C::kPer == 0) ok = ok && wait_or_abort(ms, &ms.v_full[st], at / kStages & 1, a.err);
+      const uint32_t vo = ((C::kPer * st + t % C::kPer) * C::kTileBytes) >> 4;
+      const uint32_t use = past.uses(t) & 1;
+#pragma unroll
+      for (int i = 0; i < C::kMT; ++i) {
+        ok = ok && wait_or_abort(ms, &ms.p_full[i][t & 1], use, a.err);
+        tc_fence_after();
+        if (lead) {
+          if (ok) {
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_f16_ts(tmem + C::kColO + D * i, tmem + kTile * (2 * i + (t & 1)) + 8 * ks,
+                         d_v + vo + ((ks * 2048) >> 4), idesc_o, (t | ks) != 0);
+          }
+          mma_commit(&ms.o_done[i][t & 1]);
+          if (i == C::kMT - 1 && (t % C::kPer == C::kPer - 1 || t == n - 1)) mma_commit(&ms.v_free[st]);
+        }
+        __syncwarp();
+      }
     }
+    if (lead) mbar_arrive(&ms.part_free[past.parts & 1]);
+    past.add(n);
   }
   // nothing may still write TMEM when it is released, even after a timeout
   if (lead) mma_commit(&ms.mma_done);
@@ -352,10 +330,10 @@ __device__ __forceinline__ uint64_t key_bits(int64_t a, int64_t b) {
 }
 
 template <int D, bool CAP, bool BIAS>
-__device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w, uint8_t* smem, Misc& ms, uint32_t tmem, int st) {
+__device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w, int count, const Past& past, uint8_t* smem,
+                                             Misc& ms, uint32_t tmem, int st) {
   using C = Cfg<D>;
   const int i = st >> 7, m_row = st & 127, G = a.group, dim = a.cache.dim;
-  if (i >= C::kMT) return;
   const int tok = w.i0 + i * w.tpt + m_row / G, head = w.kvh * G + m_row % G;
   const bool real = m_row < w.tpt * G && tok < w.r.rows();
   const int64_t row = w.r.r0 + tok;
@@ -408,17 +386,18 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
   const uint32_t o_addr = lane_addr + C::kColO + D * i;
   float m = -FLT_MAX, l = 0.f;
 
-  for (int t = 0; t < w.count; ++t) {
-    const int u = t >> 1, sb = t % (2 * kPairBufs), t0 = w.tile(t) * kTile;
+  for (int t = 0; t < count; ++t) {
+    const uint32_t pair = past.pairs + (t >> 1), sb = 2 * (pair % kPairBufs) + (t & 1), use = past.uses(t) & 1;
     const uint32_t s_addr = lane_addr + kTile * (2 * i + (t & 1));
-    wait_or_abort(ms, &ms.at_full[u % kPairBufs], (u / kPairBufs) & 1, a.err);
+    wait_or_abort(ms, &ms.at_full[pair % kPairBufs], (pair / kPairBufs) & 1, a.err);
     // what turns the accumulator's 16 columns into scores in log2 units, before the cap; not 0, so
     // that it leaves -inf alone
     const float4 ks4 = *reinterpret_cast<const float4*>(ms.ks[sb]);
     const float f[kGroups] = {fmaxf(fac * ks4.x, FLT_MIN), fmaxf(fac * ks4.y, FLT_MIN), fmaxf(fac * ks4.z, FLT_MIN),
                               fmaxf(fac * ks4.w, FLT_MIN)};
+    const int t0 = ms.t0[sb];
     const bool plain = ms.plain[sb];
-    wait_or_abort(ms, &ms.s_full[i][t & 1], u & 1, a.err);
+    wait_or_abort(ms, &ms.s_full[i][t & 1], use, a.err);
     tc_fence_after();
     float x[kTile];
 #pragma unroll
@@ -481,7 +460,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
       l *= alpha;
       if (t > 0) {
         // O holds exactly the tiles before t once O(t-1) is complete
-        wait_or_abort(ms, &ms.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1, a.err);
+        wait_or_abort(ms, &ms.o_done[i][(t - 1) & 1], past.uses(t - 1) & 1, a.err);
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
@@ -542,23 +521,23 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     tmem_wait_st();
     tc_fence_before();
     mbar_arrive(&ms.p_full[i][t & 1]);
-    if (t & 1) {  // the pair's scales are read
+    if ((t & 1) || t == count - 1) {  // the pair's scales are read
       __syncwarp();
-      if ((st & 31) == 0) mbar_arrive(&ms.at_free[u % kPairBufs]);
+      if ((st & 31) == 0) mbar_arrive(&ms.at_free[pair % kPairBufs]);
     }
   }
 
   // ---- result
-  if (w.count > 0) wait_or_abort(ms, &ms.o_done[i][(w.count - 1) & 1], ((w.count - 1) >> 1) & 1, a.err);
+  if (count > 0) wait_or_abort(ms, &ms.o_done[i][(count - 1) & 1], past.uses(count - 1) & 1, a.err);
   tc_fence_after();
   const bool part = a.n_splits > 1;  // one of several shares of the keys: O and l as they are
-  const float inv = part ? ms.v_max : l == 0.f ? 0.f : ms.v_max / l;
-  const int64_t slot = part_slot<D>(gridDim.x, w.x, w.kvh, blockIdx.z, a.n_splits) + st;
+  const float inv = part ? w.v_max : l == 0.f ? 0.f : w.v_max / l;
+  const int64_t slot = part_slot<D>(a.parts_x, w.x, w.kvh, w.split, a.n_splits) + st;
   uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (row * a.heads + head) * dim;
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     float o[16];
-    if (w.count > 0) {
+    if (count > 0) {
       tmem_ld16(o_addr + 16 * c, o);
       tmem_wait_ld();
     }
@@ -574,7 +553,7 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     }
     uint32_t z[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) z[k] = w.count > 0 ? f32x2_to_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+    for (int k = 0; k < 8; ++k) z[k] = count > 0 ? f32x2_to_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
     if (a.out_vec) {
       reinterpret_cast<uint4*>(out + 16 * c)[0] = make_uint4(z[0], z[1], z[2], z[3]);
       reinterpret_cast<uint4*>(out + 16 * c)[1] = make_uint4(z[4], z[5], z[6], z[7]);
@@ -590,29 +569,147 @@ __device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, const Part& w
     a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
   }
   tc_fence_before();
+  mbar_arrive(&ms.o_free[i]);
 }
 
-// The part of the grid's x for key head blockIdx.y: with T tokens a CTA and f(b) = row_start[b] / T + b,
-// request b owns the x in [f(b), f(b + 1)), at least rows / T + 1 of them.  False: no rows there, or
-// the few-row kernel's.  Called by whole warps, after which `owner` needs a barrier.
+template <int D, bool CAP, bool BIAS>
+__device__ __forceinline__ void softmax_role(const Kv8AttnArgs& a, uint8_t* smem, Misc& ms, uint32_t tmem, int st) {
+  if ((st >> 7) >= Cfg<D>::kMT) return;
+  Past past;
+  while (const Part* next = next_part(ms, past, a.err)) {
+    const Part& w = *next;
+    const int count = w.count;
+    softmax_part<D, CAP, BIAS>(a, w, count, past, smem, ms, tmem, st);
+    __syncwarp();
+    if ((st & 31) == 0) mbar_arrive(&ms.part_free[past.parts & 1]);
+    past.add(count);
+  }
+}
+
+// ------------------------------------------------------------------ parts, addresses and scales
+
+// Part x of key head kvh: with T tokens a part and f(b) = row_start[b] / T + b, request b owns the x in
+// [f(b), f(b + 1)), at least rows / T + 1 of them.  False: no rows there, or the few-row kernel's.
+// Called by a whole warp.
 template <int D>
-__device__ __forceinline__ bool find_part(const Kv8AttnArgs& a, int64_t x, int32_t& owner, Part& w) {
+__device__ __forceinline__ bool find_part(const Kv8AttnArgs& a, int64_t x, int kvh, Part& w) {
   w.tpt = kM / a.group;
   const int T = Cfg<D>::kMT * w.tpt;
   auto first_x = [&](int b) { return (int64_t)a.row_start[b] / T + b; };
-  if (threadIdx.x < 32) {
-    const int b = warp_last_le(a.bt.num_seqs, x, first_x);
-    if (threadIdx.x == 0) owner = b;
-  }
-  __syncthreads();
-  w.b = owner;
-  w.kvh = blockIdx.y;
+  w.b = warp_last_le(a.bt.num_seqs, x, first_x);
+  w.kvh = kvh;
   w.x = (int32_t)x;
   if (!kv8_request(a.row_start, a.cached, w.b, a.n_rows, a.bt, a.cache.rows_per_block, w.r, a.err)) return false;
   const int n_new = w.r.rows();
   if ((int64_t)n_new * a.group <= a.few_cols || n_new > a.max_new || x < first_x(w.b)) return false;
   w.i0 = (int)min((x - first_x(w.b)) * T, (int64_t)n_new);
   return w.i0 < n_new;
+}
+
+// One warp hands the parts out, as the CTAs come to them (an order that no result depends on), and
+// runs ahead of the other roles: what the part sees, then, 16 tokens a lane and four pairs of
+// tiles at a time, where the keys are, their scales, and which tiles need no mask.
+template <int D>
+__device__ __forceinline__ void look_up_role(const Kv8AttnArgs& a, Misc& ms) {
+  const int lane = threadIdx.x & 31, g = lane % kGroups, P = a.cache.rows_per_block, shift = 31 - __clz(P);
+  const int Hk = a.cache.kv_heads;
+  const int64_t total = (int64_t)a.parts_x * Hk * a.n_splits;
+  Past past;
+  for (;;) {
+    int64_t id = 0;
+    if (lane == 0) id = atomicAdd(a.part_next, 1);
+    id = __shfl_sync(0xffffffffu, (int)id, 0);
+    Part w{};
+    w.end = id >= total;
+    if (!w.end) {
+      // parts that see more keys go first
+      if (!find_part<D>(a, a.parts_x - 1 - id % a.parts_x, (int)(id / a.parts_x % Hk), w)) continue;
+      w.split = (int32_t)(id / a.parts_x / Hk);
+      const int last = min(w.r.rows(), w.i0 + Cfg<D>::kMT * w.tpt) - 1;  // token
+      w.n = w.r.len();
+      w.pre = a.mask.prefix ? min(a.mask.prefix[w.b], w.n) : 0;
+      if (a.mask.first) {
+        int32_t low = INT32_MAX, high = 0;
+        for (int i = w.i0 + lane; i <= last; i += 32) {
+          const int32_t f = max(a.mask.first[w.r.r0 + i], 0);
+          low = min(low, f);
+          high = max(high, f);
+        }
+        w.first = __reduce_min_sync(0xffffffffu, low);
+        w.all_first = __reduce_max_sync(0xffffffffu, high);
+      }
+      w.all_p = w.r.cached + w.i0;
+      w.all_lo = a.mask.window > 0 ? max(w.all_first, w.r.cached + last - a.mask.window + 1) : w.all_first;
+      const int lo = a.mask.window > 0 ? max(w.first, w.r.cached + w.i0 - a.mask.window + 1) : w.first;
+      w.tiles = kv8_tiles(kTile, w.first, w.pre, lo, w.r.cached + last);
+      const int64_t all = w.tiles.count();
+      w.begin = (int32_t)(all * w.split / a.n_splits);
+      w.count = (int32_t)(all * (w.split + 1) / a.n_splits) - w.begin;
+      float top = kKv8MinScale;
+      for (int part = 0; part < 2; ++part) {
+        const int i0 = part ? max(w.begin, w.tiles.nA) : w.begin;
+        const int nt = (part ? w.begin + w.count : min(w.begin + w.count, w.tiles.nA)) - i0, t0 = w.tiles.at(i0) * kTile;
+        const int lb1 = (min(w.n, t0 + nt * kTile) + P - 1) >> shift;
+        if (nt > 0)
+#pragma unroll 4
+          for (int lb = (t0 >> shift) + lane; lb < lb1; lb += 32) {
+            const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, lb);
+            if (blk >= 0) top = fmaxf(top, a.cache.v_scale[(int64_t)blk * Hk + w.kvh]);
+          }
+      }
+      w.v_max = warp_max(top);
+    }
+    const uint32_t slot = past.parts & 1;
+    if (past.parts >= 2 && !wait_or_abort(ms, &ms.part_free[slot], ((past.parts >> 1) - 1) & 1, a.err)) return;
+    if (lane == 0) {
+      ms.part[slot] = w;
+      mbar_arrive(&ms.part_full[slot]);
+    }
+    if (w.end) return;
+    const float inv_top = 1.0f / w.v_max;
+    for (int u0 = 0; 2 * u0 < w.count; u0 += 4) {
+      const int t = 2 * u0 + lane / kGroups, sb = (int)((past.pairs + (t >> 1)) % kPairBufs) * 2 + (t & 1);
+      float ks = -1.f, vs = 1.f;
+      int64_t src = -1;
+      if (t < w.count) {
+        const int tok = w.tile(t) * kTile + 16 * g;
+        if (tok < w.n) {
+          const int32_t blk = kv8_block(a.bt, a.cache.num_blocks, w.b, tok >> shift);
+          if (blk >= 0) {
+            const int64_t at = (int64_t)blk * Hk + w.kvh;
+            src = (at * P + (tok & (P - 1))) * a.cache.dim;
+            ks = a.cache.k_scale[at];
+            vs = a.cache.v_scale[at];
+          } else {
+            record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
+          }
+        }
+      }
+      for (int u = u0; u < u0 + 4 && 2 * u < w.count; ++u) {
+        const uint32_t at = past.pairs + u;
+        if (at >= kPairBufs) wait_or_abort(ms, &ms.at_free[at % kPairBufs], (at / kPairBufs - 1) & 1, a.err);
+      }
+      if (t < w.count) {
+        if (src >= 0) vs = fmaxf(vs * inv_top, kKv8MinScale);
+        ms.src[sb][g] = src;
+        ms.ks[sb][g] = ks;
+        ms.lv[sb][g] = log2f(vs);
+        ms.rv[sb][g] = 1.0f / vs;
+      }
+      // of the four lanes of a tile: all of its tokens are there, and no row's mask cuts it
+      const uint32_t there = __ballot_sync(0xffffffffu, src >= 0);
+      if (t < w.count && g == 0) {
+        const int t0 = w.tile(t) * kTile;
+        ms.t0[sb] = t0;
+        ms.plain[sb] = (there >> lane & 15u) == 15u && t0 + kTile <= w.n && t0 >= w.all_first &&
+                       ((t0 >= w.all_lo && t0 + kTile - 1 <= w.all_p) || t0 + kTile <= w.pre);
+      }
+      __syncwarp();
+      if (lane == 0)
+        for (int u = u0; u < u0 + 4 && 2 * u < w.count; ++u) mbar_arrive(&ms.at_full[(past.pairs + u) % kPairBufs]);
+    }
+    past.add(w.count);
+  }
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -640,51 +737,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
       mbar_init(&ms.at_full[u], 1);
       mbar_init(&ms.at_free[u], C::kMT * 4);
     }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&ms.part_full[k], 1);
+      mbar_init(&ms.part_free[k], C::kMT * 4 + kConvert / 32 + 1);  // the warps of the softmax, of the conversion, the products'
+      mbar_init(&ms.o_free[k], 128);
+    }
     mbar_init(&ms.q_full, C::kMT * 128);
     mbar_init(&ms.mma_done, 1);
     ms.abort = 0;
-    ms.v_max = 1.f;
     mbar_init_fence();
   }
+  if (wid == kMmaWarp) tmem_alloc(&ms.tmem_base, 512);
   pdl_trigger();
   pdl_wait();
-
-  // ---- the CTA's part; later parts see more keys and go first
-  Part w{};
-  if (!find_part<D>(a, gridDim.x - 1 - blockIdx.x, ms.owner, w)) return;
-  const int n_new = w.r.rows(), T = C::kMT * w.tpt;
-  const int last = min(n_new, w.i0 + T) - 1;  // token
-  w.n = w.r.len();
-  w.pre = a.mask.prefix ? min(a.mask.prefix[w.b], w.n) : 0;
-  if (a.mask.first) {
-    int32_t low = INT32_MAX, high = 0;
-    for (int i = w.i0 + (tid & 31); i <= last; i += 32) {
-      const int32_t f = max(a.mask.first[w.r.r0 + i], 0);
-      low = min(low, f);
-      high = max(high, f);
-    }
-    w.first = __reduce_min_sync(0xffffffffu, low);
-    w.all_first = __reduce_max_sync(0xffffffffu, high);
-  }
-  w.all_p = w.r.cached + w.i0;
-  w.all_lo = a.mask.window > 0 ? max(w.all_first, w.r.cached + last - a.mask.window + 1) : w.all_first;
-  const int lo = a.mask.window > 0 ? max(w.first, w.r.cached + w.i0 - a.mask.window + 1) : w.first;
-  w.tiles = kv8_tiles(kTile, w.first, w.pre, lo, w.r.cached + last);
-  const int64_t all = w.tiles.count();
-  w.begin = (int32_t)(all * blockIdx.z / a.n_splits);
-  w.count = (int32_t)(all * (blockIdx.z + 1) / a.n_splits) - w.begin;
-
-  if (wid == kMmaWarp) tmem_alloc(&ms.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
   if (wid < kSoftmax / 32) {
-    softmax_role<D, CAP, BIAS>(a, w, smem, ms, tmem, tid);
+    softmax_role<D, CAP, BIAS>(a, smem, ms, tmem, tid);
   } else {
-    if (wid < kMmaWarp) convert_role<D>(a, w, smem, ms, tid - kSoftmax);
-    else if (wid == kLookWarp) look_up_role(a, w, ms);
-    else mma_role<D>(a, w, smem, ms, tmem);
+    if (wid < kMmaWarp) convert_role<D>(a, smem, ms, tid - kSoftmax);
+    else if (wid == kLookWarp) look_up_role<D>(a, ms);
+    else mma_role<D>(a, smem, ms, tmem);
   }
   __syncthreads();
   tc_fence_after();
@@ -694,16 +769,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
 // Joins the shares of the keys, a warp a row.
 template <int D>
 __global__ void __launch_bounds__(128) kv8_prefill_join_kernel(const Kv8AttnArgs a) {
-  __shared__ int32_t owner;
   pdl_trigger();
   pdl_wait();
   Part w{};
-  if (!find_part<D>(a, blockIdx.x, owner, w)) return;
+  if (!find_part<D>(a, blockIdx.x, blockIdx.y, w)) return;
   const int lane = threadIdx.x & 31, G = a.group, dim = a.cache.dim, S = a.n_splits;
   const int st = blockIdx.z * 4 + (threadIdx.x >> 5), m_row = st & (kM - 1);
   const int tok = w.i0 + (st / kM) * w.tpt + m_row / G, head = w.kvh * G + m_row % G;
   if (m_row >= w.tpt * G || tok >= w.r.rows()) return;
-  auto slot = [&](int s) { return part_slot<D>(gridDim.x, w.x, w.kvh, s, S) + st; };
+  auto slot = [&](int s) { return part_slot<D>(a.parts_x, w.x, w.kvh, s, S) + st; };
   float m = -FLT_MAX;
   for (int s = 0; s < S; ++s) m = fmaxf(m, a.part_ml[2 * slot(s)]);
   float l = 0.f, o[D / 32];
@@ -725,6 +799,8 @@ __global__ void __launch_bounds__(128) kv8_prefill_join_kernel(const Kv8AttnArgs
   if (a.lse && lane == 0) a.lse[rh] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2;
 }
 
+constexpr int kSms = 152;  // of a GB300
+
 // The head size of the kernel that takes `dim`.
 int32_t tile_dim(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
@@ -744,11 +820,12 @@ cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t s) {
     return err;
   });
   if (e != cudaSuccess) return e;
-  const unsigned gx = (unsigned)grid_x(a.n_rows, a.bt.num_seqs, a.group, D), hk = (unsigned)a.cache.kv_heads;
-  const cudaError_t k = launch_k(kv8_prefill_kernel<D, CAP, BIAS>, dim3(gx, hk, a.n_splits), dim3(kThreads),
-                                 smem_bytes<D>(), s, 0, a);
+  const int64_t parts = (int64_t)a.parts_x * a.cache.kv_heads * a.n_splits;
+  const cudaError_t k = launch_k(kv8_prefill_kernel<D, CAP, BIAS>, dim3((unsigned)std::min<int64_t>(parts, kSms)),
+                                 dim3(kThreads), smem_bytes<D>(), s, 0, a);
   if (k != cudaSuccess || a.n_splits == 1) return k;
-  return launch_k(kv8_prefill_join_kernel<D>, dim3(gx, hk, Cfg<D>::kMT * kM / 4), dim3(128), 0, s, 0, a);
+  return launch_k(kv8_prefill_join_kernel<D>, dim3(a.parts_x, a.cache.kv_heads, Cfg<D>::kMT * kM / 4), dim3(128), 0, s,
+                  0, a);
 }
 
 template <int D>
@@ -757,8 +834,6 @@ cudaError_t launch_dim(const Kv8AttnArgs& a, cudaStream_t s) {
   if (cap) return bias ? launch<D, true, true>(a, s) : launch<D, true, false>(a, s);
   return bias ? launch<D, false, true>(a, s) : launch<D, false, false>(a, s);
 }
-
-constexpr int kSms = 152;  // of a GB300
 
 }  // namespace
 
@@ -784,10 +859,10 @@ size_t kv8_prefill_workspace(int32_t n_rows, int32_t num_seqs, int32_t heads, in
 }
 
 void kv8_prefill_parts(Kv8AttnArgs& a, void* ws) {
+  a.parts_x = (int32_t)grid_x(a.n_rows, a.bt.num_seqs, a.group, a.cache.dim);
   const int32_t D = tile_dim(a.cache.dim), rows = (D == 256 ? Cfg<256>::kMT : Cfg<128>::kMT) * kM;
   a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = a.part_o + (size_t)grid_x(a.n_rows, a.bt.num_seqs, a.group, a.cache.dim) * a.cache.kv_heads *
-                             a.n_splits * rows * D;
+  a.part_ml = a.part_o + (size_t)a.parts_x * a.cache.kv_heads * a.n_splits * rows * D;
 }
 
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t s) {
