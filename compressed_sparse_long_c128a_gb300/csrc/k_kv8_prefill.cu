@@ -403,29 +403,26 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) tmem_ld16(s_addr + 16 * g, x + 16 * g);
     tmem_wait_ld();
-    if constexpr (BIAS) {
+    if (CAP && (BIAS || !plain)) {  // the cap comes before a bias, and -inf would not pass it
+      bool small = true;
 #pragma unroll
-      for (int k = 0; k < kTile; ++k) {
-        float y = x[k] * f[k / 16];
-        if constexpr (CAP) y = post * tanh_exp2(y);
-        x[k] = y - slope * fabsf((float)(p - t0) - (float)k);
+      for (int k = 0; k < kTile; ++k) small &= fabsf(x[k]) * f[k / 16] <= 2.0f * kLog2e;
+      small = __all_sync(0xffffffffu, small);
+#pragma unroll
+      for (int k = 0; k < kTile; k += 2) {
+        float2 y = mul2(make_float2(x[k], x[k + 1]), make_float2(f[k / 16], f[k / 16]));
+        y = small ? tanh_small2(mul2(y, make_float2(0.5f / kLog2e, 0.5f / kLog2e)))
+                  : make_float2(tanh_exp2(y.x), tanh_exp2(y.y));
+        x[k] = post * y.x;
+        x[k + 1] = post * y.y;
       }
     }
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int k = 0; k < kTile; ++k)
+        x[k] = (CAP ? x[k] : x[k] * f[k / 16]) - slope * fabsf((float)(p - t0) - (float)k);
+    }
     if (!plain) {
-      if constexpr (CAP && !BIAS) {  // -inf would not pass the cap: it comes first
-        bool small = true;
-#pragma unroll
-        for (int k = 0; k < kTile; ++k) small &= fabsf(x[k]) * f[k / 16] <= 2.0f * kLog2e;
-        small = __all_sync(0xffffffffu, small);
-#pragma unroll
-        for (int k = 0; k < kTile; k += 2) {
-          float2 y = mul2(make_float2(x[k], x[k + 1]), make_float2(f[k / 16], f[k / 16]));
-          y = small ? tanh_small2(mul2(y, make_float2(0.5f / kLog2e, 0.5f / kLog2e)))
-                    : make_float2(tanh_exp2(y.x), tanh_exp2(y.y));
-          x[k] = post * y.x;
-          x[k + 1] = post * y.y;
-        }
-      }
       // a bit for each key that the row sees
       uint64_t see = key_bits(lo - t0, (int64_t)p + 1 - t0) | key_bits(first - t0, w.pre - t0);
       see &= key_bits(first - t0, w.n - t0);

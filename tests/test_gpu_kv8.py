@@ -262,9 +262,10 @@ def test_attn_types_strides_and_scale():
 @pytest.mark.parametrize("new", [2, 150])
 def test_caps_near_and_far_above_the_scores(new, softcap):
     b = Batch([400, 3], [new, new], 8, 2, 128, 64, BF, seed=13)
-    out, lse, st = b.attn(softcap=softcap)
-    assert st == csa.OK
-    b.check(out, lse, softcap=softcap)
+    for slopes in (None, _slopes(8)):
+        out, lse, st = b.attn(softcap=softcap, slopes=slopes)
+        assert st == csa.OK
+        b.check(out, lse, softcap=softcap, slopes=slopes)
     c = Batch([60], [7], 4, 2, 80, 32, F32, seed=13)
     out, lse, st = c.attn(softcap=softcap)
     assert st == csa.OK
