@@ -359,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NB>()) kv8_decode_ker
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[nb][i] *= fac[nb][i & 1] * mul;
       if (cap) {
-        bool small = true;  // of at most the cap in magnitude: 9e-8 of themselves off, not of the cap
+        bool small = true;  // for tanh_small2, whose error goes by the score and not by the cap
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) small &= fabsf(sc[nb][i]) <= 2.0f * kLog2e;
+          for (int i = 0; i < 4; ++i) small &= fabsf(sc[nb][i]) <= kTanhSmall * 2.0f * kLog2e;
         small = __all_sync(0xffffffffu, small);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {

@@ -406,7 +406,7 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
     if (CAP && (BIAS || !plain)) {  // the cap comes before a bias, and -inf would not pass it
       bool small = true;
 #pragma unroll
-      for (int k = 0; k < kTile; ++k) small &= fabsf(x[k]) * f[k / 16] <= 2.0f * kLog2e;
+      for (int k = 0; k < kTile; ++k) small &= fabsf(x[k]) * f[k / 16] <= kTanhSmall * 2.0f * kLog2e;
       small = __all_sync(0xffffffffu, small);
 #pragma unroll
       for (int k = 0; k < kTile; k += 2) {
@@ -434,7 +434,7 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
     }
     // the cap rises with the accumulator: without a bias or a mask only the maximum is capped here
     float mt = -INFINITY;
-    bool small = true;  // scores of at most the cap in magnitude, before it
+    bool small = true;  // scores that tanh_small2 takes
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float* y = x + 16 * g;
@@ -447,7 +447,7 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = fminf(fminf(y[k], y[k + 4]), fminf(y[k + 8], y[k + 12]));
         const float low = fminf(fminf(z[0], z[1]), fminf(z[2], z[3]));
-        small &= fmaxf(top, -low) * f[g] <= 2.0f * kLog2e;
+        small &= fmaxf(top, -low) * f[g] <= kTanhSmall * 2.0f * kLog2e;
       }
     }
     small = CAP && !BIAS && __all_sync(0xffffffffu, small);
