@@ -73,6 +73,12 @@ def test_plan_without_slots_or_free_blocks():
     assert (slot == -7).all()
 
 
+def test_plan_of_no_requests():
+    (table, starts, seq, pos, slot, used), status = _run_plan(np.zeros(0), np.zeros(0), [5], np.zeros((0, 2)), 16, 8, 3)
+    assert status == csa.OK and starts.tolist() == [0] and used[0] == 0
+    assert seq.tolist() == pos.tolist() == slot.tolist() == [-1] * 3
+
+
 def test_plan_reports_what_does_not_fit():
     # too few free blocks: request 1 gets one of the two it needs
     (table, _, seq, pos, slot, used), status = _run_plan([0, 0], [16, 32], [5, 6], [[0, 0, 0], [0, 0, 0]], 16, 8, 48)
@@ -236,6 +242,24 @@ def test_attn_matches_the_oracle(shape, mask):
         m["first"] = np.concatenate([first, np.zeros(b.rows - b.T, np.int64)])
     out, lse, status = b.attn(**m)
     assert status == csa.OK
+    b.check(out, lse, **m)
+
+
+@pytest.mark.parametrize("dim,cap,docs", [(64, 0.0, True), (128, 0.0, False), (128, 5.0, True), (256, 0.0, True), (96, 0.0, False)])
+def test_more_parts_than_sms(dim, cap, docs):
+    """Prompts by the dozen, short and long, single tokens and nothing among them: every CTA goes through
+    several parts, some of which see nothing."""
+    r = np.random.RandomState(60)
+    cached, new = r.randint(0, 400, 70), r.choice([0, 1, 3, 20, 64, 65, 129], 70)
+    b = Batch(cached, new, 16, 4, dim, 32, BF, seed=60)
+    m = {"softcap": cap, "window": 150}
+    if docs:
+        first = r.randint(0, 500, b.rows)
+        first[r.random_sample(b.rows) < 0.3] = 10 ** 6
+        first[b.start[5]:b.start[6]] = first[b.start[9]:b.start[10]] = 10 ** 6
+        m["first"] = first
+    out, lse, st = b.attn(**m)
+    assert st == csa.OK
     b.check(out, lse, **m)
 
 
@@ -424,6 +448,84 @@ def test_captured_step_follows_its_inputs():
             got = torch.full((b.rows, H, D), 7.0, dtype=BF)
             got[: b.T] = s["out"][: b.T].cpu()
             b.check(got, None)
+
+
+def test_whole_step_captured():
+    """Plan, insert and attention in one graph, replayed for steps of other lengths; rows behind a step's
+    last one keep what they held."""
+    B, H, Hk, D, P, blocks, cap, most = 3, 8, 2, 64, 16, 60, 130, 64
+    r = np.random.RandomState(70)
+    i32 = torch.int32
+    cache, err = csa.Kv8Cache.empty(blocks, Hk, P, D), _err()
+    cd, nd, start, used = (torch.zeros(n, dtype=i32, device="cuda") for n in (B, B, B + 1, 1))
+    seq, pos = (torch.zeros(cap, dtype=i32, device="cuda") for _ in range(2))
+    slot = torch.zeros(cap, dtype=torch.int64, device="cuda")
+    free, table = torch.zeros(blocks, dtype=i32, device="cuda"), torch.full((B, 20), -1, dtype=i32, device="cuda")
+    qkv = torch.zeros(cap, H + 2 * Hk, D, dtype=BF, device="cuda")
+    out = torch.zeros(cap, H, D, dtype=BF, device="cuda")
+    ws = torch.empty(csa.kv8_attn_workspace_size(cap, B, H, cache, most), dtype=torch.uint8, device="cuda")
+
+    def step():
+        csa.step_plan(cd, nd, free, table, P, blocks, start, seq, pos, slot, used, err)
+        csa.kv8_store(qkv[:, H:H + Hk], qkv[:, H + Hk:], start, cd, cache, table, err)
+        csa.kv8_attn(qkv[:, :H], start, cd, cache, table, most, out, ws, err, softcap=20.0)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        step()
+    ok = [np.zeros((blocks, Hk, P, D), np.uint8) for _ in range(2)]
+    os_ = [np.zeros((blocks, Hk), np.float32) for _ in range(2)]
+    ids, cached = list(r.permutation(blocks)), np.zeros(B, np.int64)
+    for new in ([50, 3, 64], [1, 0, 1], [0, 40, 1], [1, 1, 1]):
+        T = int(np.sum(new))
+        x = stored(r.standard_normal((cap, H + 2 * Hk, D)), BF)
+        qkv.copy_(x), out.fill_(7), cd.copy_(dev(cached)), nd.copy_(dev(new))
+        free[: len(ids)].copy_(dev(ids))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert csa.read_status(err) == csa.OK
+        ids = ids[int(used):]
+        st, t = start.cpu().numpy(), table.cpu().numpy()
+        assert np.array_equal(st, np.concatenate([[0], np.cumsum(new)])) and (pos[T:] == -1).all()
+        for i in range(2):
+            ok[i], os_[i] = K.store(x[:, H + i * Hk:H + (i + 1) * Hk].float().numpy(), st, cached, t, ok[i], os_[i])
+        assert np.array_equal(cache.k.cpu().numpy(), ok[0]) and np.array_equal(cache.v.cpu().numpy(), ok[1])
+        got = out.double().cpu().numpy()
+        assert (got[T:] == 7).all()
+        for b in range(B):
+            if not new[b]:
+                continue
+            p, n = cached[b] + np.arange(new[b]), int(cached[b] + new[b])
+            for h in range(Hk):
+                kk, vv = (K.gather(ok[i], os_[i], t[b], n, h) for i in range(2))
+                want, _, wabs, _ = K.attend(x[st[b]:st[b + 1], 4 * h:4 * h + 4].double().numpy(), kk, vv, p,
+                                            K.sees(p, n, np.zeros(new[b]), 0, 0), D ** -0.5, 20.0)
+                assert np.all(np.abs(got[st[b]:st[b + 1], 4 * h:4 * h + 4] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * wabs)
+        cached = cached + np.array(new)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with a workspace of its own, give what they give alone."""
+    bs = [Batch([3000, 17, 900], [1, 1, 2], 16, 2, 128, 64, BF, seed=80), Batch([400, 30], [200, 90], 16, 2, 128, 64, BF, seed=81)]
+    alone = [b.attn()[:2] for b in bs]
+    streams, state = [torch.cuda.Stream() for _ in bs], []
+    for b in bs:
+        c = b.cache()
+        n = csa.kv8_attn_workspace_size(b.rows, b.B, b.H, c, b.max_new)
+        state.append((b.q.cuda(), dev(b.start), dev(b.cached), c, dev(b.table), b.max_new,
+                      torch.full((b.rows, b.H, b.D), 7.0, dtype=BF, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda"), _err()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, a in zip(streams, state):
+            csa.kv8_attn(*a, stream=s)
+    torch.cuda.synchronize()
+    for a, want in zip(state, alone):
+        assert csa.read_status(a[-1]) == csa.OK and torch.equal(a[6].cpu(), want[0])
 
 
 def test_offsets_past_32_bits():
