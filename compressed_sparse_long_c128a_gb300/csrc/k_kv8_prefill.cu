@@ -364,7 +364,7 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
     const int lane = st & 31, piece = lane % kLanes, sub = lane / kLanes, row0 = m_row - lane;
     // a row's offset, or -1, from the lane that holds it
     const int64_t mine = real ? row * a.q_stride + (int64_t)head * dim : -1;
-#pragma unroll
+#pragma unroll 1
     for (int c0 = 0; c0 < 32 / kRows; c0 += 8) {
       uint4 v[8];
 #pragma unroll
