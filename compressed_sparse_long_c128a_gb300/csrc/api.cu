@@ -456,7 +456,7 @@ size_t csa_kv8_attn_workspace_size(int32_t n_rows, int32_t num_seqs, int32_t hea
   // the types decide between the kernels, which run one after the other; size for the largest
   const int32_t kv = cache->kv_heads, dim = cache->dim;
   if (heads < kv) return 0;
-  const Kv8Plan p = kv8_plan(heads / kv, max_new);
+  const Kv8Plan p = kv8_plan(heads / kv, std::min(max_new, n_rows));
   size_t most = std::max(kv8_simt_workspace(n_rows, heads, dim, kv8_simt_splits(n_rows, heads, kv)),
                          kv8_decode_workspace(dim, p.cols));
   if (p.many)
@@ -506,16 +506,23 @@ int csa_kv8_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_row
   if (q_dtype == CSA_BF16 && out_dtype == CSA_BF16) {
     a.q_vec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_stride % 8 == 0;
     a.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    const Kv8Plan p = kv8_plan(a.group, max_new);
-    a.cols = p.cols;
-    a.few_cols = p.few_cols;
-    a.part_next = reinterpret_cast<int32_t*>(ws);
+    const Kv8Plan p = kv8_plan(a.group, std::min(max_new, n_rows));
+    const int64_t max_len = (int64_t)bt->stride * cache->rows_per_block;  // what the table can map
     void* parts = reinterpret_cast<uint8_t*>(ws) + kKv8Head;
-    kv8_decode_parts(a, parts);
-    if (launch_kv8_decode(a, stream) != cudaSuccess) return CSA_ERR_CUDA;
-    if (!p.many) return CSA_OK;
-    a.n_splits = kv8_prefill_splits(n_rows, bt->num_seqs, heads, cache->kv_heads, cache->dim,
-                                    (int64_t)bt->stride * cache->rows_per_block);
+    if (p.many && bt->num_seqs == 1) {
+      // one prompt: no single tokens beside it, and two launches less.  (A padded call that turns out to hold
+      // a single token is the loser: it gets 16 CTAs a key head and not the whole GPU.)
+      a.few_cols = 0;
+    } else {
+      a.cols = p.cols;
+      a.few_cols = p.few_cols;
+      a.part_next = reinterpret_cast<int32_t*>(ws);
+      a.whole_pairs = max_len <= 256;
+      kv8_decode_parts(a, parts);
+      if (launch_kv8_decode(a, stream) != cudaSuccess) return CSA_ERR_CUDA;
+      if (!p.many) return CSA_OK;
+    }
+    a.n_splits = kv8_prefill_splits(n_rows, bt->num_seqs, heads, cache->kv_heads, cache->dim, max_len);
     kv8_prefill_parts(a, parts);
     return cuda_status(launch_kv8_prefill(a, stream));
   }

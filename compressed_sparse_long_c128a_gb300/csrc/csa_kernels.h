@@ -316,9 +316,11 @@ struct Kv8AttnArgs {
   float* part_o;  // partial results, see the kernels
   float* part_ml;
   int32_t* part_head;
-  int32_t* part_next;  // the many-row kernel's next part; the few-row kernel before it sets it to 0
+  int32_t* part_next;  // the many-row kernel's next part, set to 0 by the few-row kernel before it; null: there
+                       // is none, and every CTA takes each gridDim-th part
   int32_t parts_x;     // parts a key head
   int32_t n_splits;
+  int32_t whole_pairs;  // the few-row kernel shares no pair between CTAs
   int32_t cols;      // query columns (rows x group) of a tile of the few-row kernel
   int32_t few_cols;  // it takes the requests of at most so many columns
   int32_t q_vec, out_vec;  // q rows and out may be accessed 16 bytes at a time

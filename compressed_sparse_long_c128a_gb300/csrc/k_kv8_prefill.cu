@@ -647,7 +647,11 @@ __device__ __forceinline__ bool find_part(const Kv8AttnArgs& a, int64_t x, int k
   w.x = (int32_t)x;
   if (!kv8_request(a.row_start, a.cached, w.b, a.n_rows, a.bt, a.cache.rows_per_block, w.r, a.err)) return false;
   const int n_new = w.r.rows();
-  if ((int64_t)n_new * a.group <= a.few_cols || n_new > a.max_new || x < first_x(w.b)) return false;
+  if (n_new > a.max_new) {
+    record_error(a.err, CSA_ERR_DEVICE_BOUNDS);
+    return false;
+  }
+  if ((int64_t)n_new * a.group <= a.few_cols || x < first_x(w.b)) return false;
   w.i0 = (int)min((x - first_x(w.b)) * T, (int64_t)n_new);
   return w.i0 < n_new;
 }
@@ -661,10 +665,13 @@ __device__ __forceinline__ void look_up_role(const Kv8AttnArgs& a, Misc& ms) {
   const int Hk = a.cache.kv_heads;
   const int64_t total = (int64_t)a.parts_x * Hk * a.n_splits;
   Past past;
-  for (;;) {
-    int64_t id = 0;
-    if (lane == 0) id = atomicAdd(a.part_next, 1);
-    id = __shfl_sync(0xffffffffu, (int)id, 0);
+  for (int64_t turn = blockIdx.x;; turn += gridDim.x) {
+    int64_t id = turn;
+    if (a.part_next) {
+      int next = 0;
+      if (lane == 0) next = atomicAdd(a.part_next, 1);
+      id = __shfl_sync(0xffffffffu, next, 0);
+    }
     Part w{};
     w.end = id >= total;
     if (!w.end) {

@@ -423,8 +423,9 @@ typedef struct {
  *   out  [n_rows][heads][dim] out_dtype (F32 or BF16); lse [n_rows][heads] float or NULL
  *   heads a multiple of kv_heads; max_new >= every request's rows
  *   row_start, cached as in csa_kv8_store
- *   ws   at least csa_kv8_attn_workspace_size(...) bytes, 16-byte aligned.  Scratch:
- *        nothing needs to start at zero, and calls that can overlap need their own.
+ *   ws   at least csa_kv8_attn_workspace_size(...) bytes for this call's sizes (fewer rows
+ *        can need more: their keys are shared out), 16-byte aligned.  Scratch: nothing needs
+ *        to start at zero, and calls that can overlap need their own.
  * With BF16 q and out, probabilities (times their block's value scale) are rounded to
  * fp16 before they meet the values: 11 bits as long as that product is within 2^-21
  * of the largest a request's rows meet, fewer below.  Otherwise everything stays in fp32.

@@ -212,6 +212,9 @@ SHAPES = [
     ([200, 77], [1, 60], 10, 2, 160, 64, BF),
     ([400], [50], 4, 4, 240, 128, BF),
     ([6000], [37], 16, 2, 128, 256, BF),
+    ([300], [3], 16, 2, 128, 64, BF),
+    ([3], [1], 16, 2, 64, 16, BF),
+    ([100, 500, 0, 0], [1, 2, 1, 0], 40, 4, 128, 64, BF),
     ([5000, 9], [90, 1], 4, 1, 64, 64, BF),
     ([4100], [50], 8, 1, 192, 32, BF),
     ([100, 7], [1, 30], 12, 4, 80, 16, F32),
@@ -330,6 +333,19 @@ def test_attn_skips_what_is_out_of_bounds(new):
     if new > 1:
         out, lse, st = b.attn(max_new=new - 1)
         assert st == csa.ERR_DEVICE_BOUNDS and (out == 7).all()
+
+
+@pytest.mark.parametrize("new", [1, 5, 150])
+def test_one_request_in_a_padded_call(new):
+    """Rows behind the request and a bound far above its rows, as a captured call of fixed shapes has."""
+    for spare, max_new in ((3, 200), (300, 400)):
+        b = Batch([700], [new], 8, 2, 128, 64, BF, seed=21, spare_rows=spare)
+        out, lse, st = b.attn(max_new=max_new)
+        assert st == csa.OK
+        b.check(out, lse)
+        if new > 1:
+            out, lse, st = b.attn(max_new=new - 1)
+            assert st == csa.ERR_DEVICE_BOUNDS and (out == 7).all() and (lse == 7).all()
 
 
 def test_nan_query_stays_in_its_row():
