@@ -5,7 +5,9 @@
 // once (copies in shared memory last from amax to the codes; what does not fit there is
 // read again), rounds the block's older rows
 // again in the rare case that the scale rose, and no two CTAs meet at a scale.
-// HBM bounds it: 2 or 4 bytes in and 1 byte out a value.
+// HBM bounds it: 2 or 4 bytes in and 1 byte out a value.  16384 bf16 rows of 8 heads of 128
+// take 24.5 us in a graph, 4.1 TB/s; what is left is that a unit's codes wait for its maximum.
+// 64 single tokens take 4.4 us: the launch and a chain of four dependent reads.
 //
 // Units are found without a list.  With f(b) = row_start[b] / P + b, request b owns the
 // units x in [f(b), f(b+1)): there are n_rows / P + num_seqs, whatever the lengths are.  A
@@ -21,10 +23,16 @@
 namespace csa {
 namespace {
 
-// Units of hundreds of rows keep 256 threads and 64 KB of copies busy, three CTAs an SM; those
-// of a few rows need neither.
-constexpr int kBigThreads = 256, kBigBytes = 65536;
-constexpr int kSmallThreads = 64, kSmallBytes = 4096;
+// Threads of a unit and the most bytes of it that stay in shared memory, with the registers
+// held to what six CTAs of 256 threads (five, fp32) can have; the rest is read again, from L2.
+// 16384 rows, 8 heads of 128, in a graph, by this rule and otherwise:
+//  * a few rows, or blocks of few: 64 threads, 4 KB (blocks of 16: 26.6 us; 31.8 with the
+//    80 registers that the compiler takes by itself);
+//  * up to 32 KB: 128 threads, 24 KB (bf16, blocks of 64: 24.4 us; 28.9 with 256 threads);
+//  * more: 256 threads, 16 KB of bf16 (blocks of 256: 24.5 us; 28.1 with all 64 KB, as only
+//    three CTAs fit an SM then) and 64 KB of fp32 (47.8 us; 52.3 with 16).
+constexpr int kFewThreads = 64, kMidThreads = 128, kBigThreads = 256;
+constexpr int kFewBytes = 4096, kMidBytes = 24576, kMostBytes = 65536, kMostBytesBf16 = 16384;
 
 // 16 values as they are stored.
 template <typename T>
@@ -100,8 +108,9 @@ __device__ __forceinline__ uint4 pack16(const float* v, float mul) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, int kThreads, int kBytes>
-__global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs a) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? (sizeof(T) == 2 ? 6 : 5) : 1280 / kThreads)
+    kv8_store_kernel(const Kv8StoreArgs a, const int room) {
   extern __shared__ __align__(16) uint8_t buf[];
   __shared__ uint32_t red[32];
   __shared__ int owner;
@@ -135,8 +144,7 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
     const T* rows = src + (int64_t)(r.r0 + p0 - r.cached) * stride;
     // the thread's pieces (16 values): as many as fit are copied to shared memory and stay there
     // between the two passes, 16 bytes of all pieces next to each other
-    constexpr int kKept = kBytes / (16 * (int)sizeof(T));
-    const int kept = a.vec ? min(m * units, kKept) : 0;
+    const int kept = a.vec ? min(m * units, room) : 0;
     auto source = [&](int u) {
       const int row = (unsigned)u / (unsigned)units;
       return rows + row * stride + (u - row * units) * 16;
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
       const T* src = source(u);
 #pragma unroll
       for (int j = 0; j < (int)sizeof(T); ++j)
-        tc::cp_async16(tc::smem_u32(buf) + (j * kKept + u) * 16, reinterpret_cast<const uint4*>(src) + j, 16);
+        tc::cp_async16(tc::smem_u32(buf) + (j * room + u) * 16, reinterpret_cast<const uint4*>(src) + j, 16);
     }
     tc::cp_async_commit();
     // (the block is looked up while the copies are on their way)
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
       Raw<T> r;
 #pragma unroll
       for (int j = 0; j < (int)sizeof(T); ++j) {
-        const uint4 x = reinterpret_cast<const uint4*>(buf)[j * kKept + u];
+        const uint4 x = reinterpret_cast<const uint4*>(buf)[j * room + u];
         r.w[4 * j] = x.x, r.w[4 * j + 1] = x.y, r.w[4 * j + 2] = x.z, r.w[4 * j + 3] = x.w;
       }
       return r;
@@ -227,31 +235,40 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const Kv8StoreArgs 
   }
 }
 
-template <typename T, int kThreads, int kBytes>
-cudaError_t launch(const Kv8StoreArgs& a, cudaStream_t s) {
+template <typename T>
+int64_t unit_bytes(const Kv8StoreArgs& a) {
+  return (int64_t)a.cache.rows_per_block * a.cache.dim * sizeof(T);
+}
+
+template <typename T, int kThreads>
+cudaError_t launch(const Kv8StoreArgs& a, int32_t most_bytes, cudaStream_t s) {
   static PerDevice attr;
   const cudaError_t e = with_device_slot(attr, [](int, int64_t& v) {
     if (v) return cudaSuccess;
-    const cudaError_t err = cudaFuncSetAttribute(kv8_store_kernel<T, kThreads, kBytes>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    const cudaError_t err = cudaFuncSetAttribute(kv8_store_kernel<T, kThreads>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
     if (err == cudaSuccess) v = 1;
     return err;
   });
   if (e != cudaSuccess) return e;
   const unsigned gx = (unsigned)(a.n_rows / a.cache.rows_per_block + a.bt.num_seqs);
-  return launch_k(kv8_store_kernel<T, kThreads, kBytes>, dim3(gx * 2 * a.cache.kv_heads), dim3(kThreads), kBytes, s, 0, a);
+  const int32_t bytes = (int32_t)std::min((int64_t)most_bytes, unit_bytes<T>(a));
+  return launch_k(kv8_store_kernel<T, kThreads>, dim3(gx * 2 * a.cache.kv_heads), dim3(kThreads), bytes, s, 0, a,
+                  bytes / (16 * (int)sizeof(T)));
+}
+
+template <typename T>
+cudaError_t pick(const Kv8StoreArgs& a, cudaStream_t s) {
+  // rows of a unit, by the average request: up to a block's, or a step's few
+  if (std::min(a.n_rows / a.bt.num_seqs, a.cache.rows_per_block) <= 16) return launch<T, kFewThreads>(a, kFewBytes, s);
+  if (unit_bytes<T>(a) <= 32768) return launch<T, kMidThreads>(a, kMidBytes, s);
+  return launch<T, kBigThreads>(a, sizeof(T) == 2 ? kMostBytesBf16 : kMostBytes, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_store(const Kv8StoreArgs& a, cudaStream_t s) {
-  // rows of a unit, by the average request: up to a block's, or a step's few
-  const int32_t mean = a.n_rows / a.bt.num_seqs;
-  const bool small = std::min(mean, a.cache.rows_per_block) <= 16;
-  if (a.in_dtype == CSA_F32)
-    return small ? launch<float, kSmallThreads, kSmallBytes>(a, s) : launch<float, kBigThreads, kBigBytes>(a, s);
-  return small ? launch<__nv_bfloat16, kSmallThreads, kSmallBytes>(a, s)
-               : launch<__nv_bfloat16, kBigThreads, kBigBytes>(a, s);
+  return a.in_dtype == CSA_F32 ? pick<float>(a, s) : pick<__nv_bfloat16>(a, s);
 }
 
 }  // namespace csa
