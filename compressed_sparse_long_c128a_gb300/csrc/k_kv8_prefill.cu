@@ -30,9 +30,12 @@
 //    divided out of each 16 columns' part of the sum.
 //  * CTAs stay, one an SM, and take parts from a queue.  The roles go from part to part on
 //    their own, so that a part's first copies are under way before the last part's result
-//    is stored: 1.37 -> 1.17 ms.
-//  * What bounds it now: 993 TFLOP/s without a cap (0.53 of the measured rate); the
-//    conversion and the softmax each need about the time that the products leave them.
+//    is stored: 1.37 -> 1.17 ms without a cap when it came in.
+//  * What bounds it now: two chunks of 2048 tokens at 4k to 16k, 64 query heads on 8 key
+//    heads of 128, take 1.27 ms without a cap, 921 TFLOP/s (0.49 of the measured rate; ncu:
+//    tensor pipe 47 % busy, issue slots 45 %), and 1.98 ms with one, 588.  The conversion
+//    and the softmax each need about the time that the products leave them, and wait for
+//    TMEM and for each other the rest of it.
 
 #include <algorithm>
 #include <cfloat>

@@ -3,8 +3,8 @@
 // A block's scale is the largest of what it was and amax / 448 over its new rows, so a
 // (request, block, head, key or value) is one unit of work: one CTA reads the unit's rows
 // once (copies in shared memory last from amax to the codes; what does not fit there is
-// read again), rounds the block's older rows
-// again in the rare case that the scale rose, and no two CTAs meet at a scale.
+// read again), rounds the block's older rows again in the rare case that the scale rose,
+// and no two CTAs meet at a scale.
 // HBM bounds it: 2 or 4 bytes in and 1 byte out a value.  16384 bf16 rows of 8 heads of 128
 // take 24.5 us in a graph, 4.1 TB/s; what is left is that a unit's codes wait for its maximum.
 // 64 single tokens take 4.4 us: the launch and a chain of four dependent reads.
