@@ -8,12 +8,14 @@
 //   S_i [128 x 64]  = Q_i [128 x D] . K^T          both operands from shared memory
 //   O_i [128 x D]  += P_i [128 x 64] . V           P from TMEM
 //
-//  * TMEM: S_0 and S_1, two buffers of 64 columns each, O_0, O_1 (D columns each), and P_i
-//    (f16, 32 columns, two buffers) behind them.  One lane issues S_0(t+1), S_1(t+1), O_0(t),
-//    O_1(t): the scores of the next tile are there when the softmax comes to them.  With
-//    heads of 128, S and O fill TMEM and P_i is written over S_i; S_i(t+1) then overwrites the
-//    P_i(t-1) that O_i(t-1) reads, and follows it because one CTA's products run in the order
-//    of issue.  (Waiting for O_i(t-1) there instead took 17 % more time.  With tiles of 128
+//  * TMEM: S_0 and S_1 (64 columns each, two buffers, one for heads of 128, which leave no
+//    room for more), O_0, O_1 (D columns each) and P_i (f16, 32 columns, two buffers).  One lane
+//    issues S_0(t+1), S_1(t+1), O_0(t), O_1(t): the scores of the next tile are there when the
+//    softmax comes to them.  S_i(t+1) waits until S_i(t) is in registers where it shares its
+//    columns.  (P_i over S_i instead, with two buffers, is 5 to 10 % faster for heads of 128, but
+//    then S_i(t+1) overwrites the P_i(t-1) that O_i(t-1) reads, and products of different shapes
+//    are not promised to run in the order of issue.  A warp for the S and one for the O
+//    took 14 % more time, the order S_0(t+1), O_1(t-1), S_1(t+1), O_0(t) 13 %; with tiles of 128
 //    keys and one S_i, each softmax waited for two products and their hand-over.)  The
 //    whole warp runs the loop, so that descriptors stay in uniform registers: issued by a
 //    lane on its own, each product cost 125 cycles.
@@ -32,8 +34,8 @@
 //    their own, so that a part's first copies are under way before the last part's result
 //    is stored: 1.37 -> 1.17 ms without a cap when it came in.
 //  * What bounds it now: two chunks of 2048 tokens at 4k to 16k, 64 query heads on 8 key
-//    heads of 128, take 1.27 ms without a cap, 921 TFLOP/s (0.49 of the measured rate; ncu:
-//    tensor pipe 47 % busy, issue slots 45 %), and 1.98 ms with one, 588.  The conversion
+//    heads of 128, take 1.26 ms without a cap, 925 TFLOP/s (0.49 of the measured rate; ncu:
+//    tensor pipe 47 % busy, issue slots 45 %), and 2.08 ms with one, 561.  The conversion
 //    and the softmax each need about the time that the products leave them, and wait for
 //    TMEM and for each other the rest of it.
 
@@ -70,13 +72,14 @@ struct Cfg {
   static constexpr uint32_t kQBytes = kQAtom * (D / 64), kTileBytes = kAtom * (D / 64);
   static constexpr uint32_t kOffK = kMT * kQBytes, kOffV = kOffK + kPer * kStages * kTileBytes;
   static constexpr uint32_t kOffMisc = kOffV + kPer * kStages * kTileBytes;
-  static constexpr uint32_t kColO = kMT * 2 * kTile;          // S_i(t) at (2 i + t % 2) kTile
+  static constexpr int kSBufs = D == 128 ? 1 : 2;  // buffers of S_i: TMEM has no more room beside two heads of 128
+  static constexpr uint32_t kColO = kMT * kSBufs * kTile;
   static constexpr int kUnits = kTile * (D / 16) / kConvert;  // 16-byte pieces of a tile a thread
-  // P_i(t): in columns of its own behind O, but for two heads of 128, whose S and O fill TMEM
-  static constexpr bool kOwnP = D != 128;
-  __host__ __device__ static constexpr uint32_t col_p(int i, int buf) {
-    return kOwnP ? kColO + kMT * D + (kTile / 2) * (2 * i + buf) : kTile * (2 * i + buf);
+  __host__ __device__ static constexpr uint32_t col_s(int i, int t) { return kTile * (kSBufs * i + t % kSBufs); }
+  __host__ __device__ static constexpr uint32_t col_p(int i, int t) {
+    return kColO + kMT * D + (kTile / 2) * (2 * i + t % 2);
   }
+  static_assert(kColO + kMT * D + kTile * kMT <= 512, "TMEM");
 };
 
 // What a CTA works on: tokens i0 .. of request b for key head kvh.
@@ -96,7 +99,7 @@ struct Part {
 struct Misc {
   uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
   // by the parity of t within its part: who waits for a tile may be one tile behind, never two
-  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
+  uint64_t s_full[2][2], s_read[2][2], p_full[2][2], o_done[2][2];
   uint64_t at_full[kPairBufs], at_free[kPairBufs], mma_done;
   // by the parity of the part: a role may be one part ahead of another (after one that sees nothing)
   uint64_t part_full[2], part_free[2], q_full[2], o_free[2][2];
@@ -281,14 +284,19 @@ __device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, uint8_t* smem, Mi
       const uint32_t at = stage0 + t / C::kPer, st = at % kStages;
       if (t % C::kPer == 0) ok = ok && wait_or_abort(ms, &ms.k_full[st], at / kStages & 1, a.err);
       const uint32_t ko = ((C::kPer * st + t % C::kPer) * C::kTileBytes) >> 4;
+      if (C::kSBufs == 1 && t > 0) {  // (two buffers: S_i(t-2) was read before P_i(t-2) came)
+#pragma unroll
+        for (int i = 0; i < C::kMT; ++i)
+          ok = ok && wait_or_abort(ms, &ms.s_read[i][(t - 1) & 1], past.uses(t - 1) & 1, a.err);
+        tc_fence_after();
+      }
       if (lead) {
 #pragma unroll
         for (int i = 0; i < C::kMT; ++i) {
           if (ok) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              mma_bf16(tmem + kTile * (2 * i + (t & 1)),
-                       d_q + ((i * C::kQBytes + (ks >> 2) * C::kQAtom + (ks & 3) * 32) >> 4),
+              mma_bf16(tmem + C::col_s(i, t), d_q + ((i * C::kQBytes + (ks >> 2) * C::kQAtom + (ks & 3) * 32) >> 4),
                        d_k + ko + (((ks >> 2) * C::kAtom + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
           }
           mma_commit(&ms.s_full[i][t & 1]);
@@ -316,7 +324,7 @@ __device__ __forceinline__ void mma_role(const Kv8AttnArgs& a, uint8_t* smem, Mi
           if (ok) {
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_f16_ts(tmem + C::kColO + D * i, tmem + C::col_p(i, t & 1) + 8 * ks, d_v + vo + ((ks * 2048) >> 4),
+              mma_f16_ts(tmem + C::kColO + D * i, tmem + C::col_p(i, t) + 8 * ks, d_v + vo + ((ks * 2048) >> 4),
                          idesc_o, (t | ks) != 0);
           }
           mma_commit(&ms.o_done[i][t & 1]);
@@ -420,7 +428,7 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
 
   for (int t = 0; t < count; ++t) {
     const uint32_t pair = past.pairs + (t >> 1), sb = 2 * (pair % kPairBufs) + (t & 1), use = past.uses(t) & 1;
-    const uint32_t s_addr = lane_addr + kTile * (2 * i + (t & 1)), p_addr = lane_addr + C::col_p(i, t & 1);
+    const uint32_t s_addr = lane_addr + C::col_s(i, t), p_addr = lane_addr + C::col_p(i, t);
     wait_or_abort(ms, &ms.at_full[pair % kPairBufs], (pair / kPairBufs) & 1, a.err);
     // what turns the accumulator's 16 columns into scores in log2 units, before the cap; not 0, so
     // that it leaves -inf alone
@@ -435,6 +443,11 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) tmem_ld16(s_addr + 16 * g, x + 16 * g);
     tmem_wait_ld();
+    if constexpr (C::kSBufs == 1) {
+      tc_fence_before();
+      __syncwarp();
+      if ((st & 31) == 0) mbar_arrive(&ms.s_read[i][t & 1]);
+    }
     if (CAP && (BIAS || !plain)) {  // the cap comes before a bias, and -inf would not pass it
       bool small = true;
 #pragma unroll
@@ -502,7 +515,7 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
         }
       }
     }
-    // ---- P over S
+    // ---- P(t), over P(t-2): O(t-2) was issued before S(t), so its product is done
     const float4 lv4 = *reinterpret_cast<const float4*>(ms.lv[sb]), rv4 = *reinterpret_cast<const float4*>(ms.rv[sb]);
     const float lv[kGroups] = {lv4.x, lv4.y, lv4.z, lv4.w}, rv[kGroups] = {rv4.x, rv4.y, rv4.z, rv4.w};
     const float shift = kPShift - m;
@@ -549,7 +562,8 @@ __device__ __forceinline__ void softmax_part(const Kv8AttnArgs& a, const Part& w
     }
     tmem_wait_st();
     tc_fence_before();
-    mbar_arrive(&ms.p_full[i][t & 1]);
+    __syncwarp();
+    if ((st & 31) == 0) mbar_arrive(&ms.p_full[i][t & 1]);
     if ((t & 1) || t == count - 1) {  // the pair's scales are read
       __syncwarp();
       if ((st & 31) == 0) mbar_arrive(&ms.at_free[pair % kPairBufs]);
@@ -785,7 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
     for (int i = 0; i < C::kMT; ++i) {
       for (int s = 0; s < 2; ++s) {
         mbar_init(&ms.s_full[i][s], 1);
-        mbar_init(&ms.p_full[i][s], 128);
+        mbar_init(&ms.s_read[i][s], 4);
+        mbar_init(&ms.p_full[i][s], 4);
         mbar_init(&ms.o_done[i][s], 1);
       }
     }
