@@ -35,7 +35,7 @@
 //    is stored: 1.37 -> 1.17 ms without a cap when it came in.
 //  * What bounds it now: two chunks of 2048 tokens at 4k to 16k, 64 query heads on 8 key
 //    heads of 128, take 1.26 ms without a cap, 925 TFLOP/s (0.49 of the measured rate; ncu:
-//    tensor pipe 47 % busy, issue slots 45 %), and 2.08 ms with one, 561.  The conversion
+//    tensor pipe 43 % busy, issue slots 43 %), and 2.08 ms with one, 561.  The conversion
 //    and the softmax each need about the time that the products leave them, and wait for
 //    TMEM and for each other the rest of it.
 
