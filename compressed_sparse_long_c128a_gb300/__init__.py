@@ -445,6 +445,7 @@ def kv8_store(k, v, row_start, cached, cache: Kv8Cache, bt, err, stream=None):
 
 
 def kv8_attn_workspace_size(n_rows: int, num_seqs: int, heads: int, cache: Kv8Cache, max_new: int) -> int:
+    """Bytes of scratch of a kv8_attn call of these sizes; a call of fewer rows can need more."""
     return int(lib().csa_kv8_attn_workspace_size(n_rows, num_seqs, heads, cache.c(), max_new))
 
 

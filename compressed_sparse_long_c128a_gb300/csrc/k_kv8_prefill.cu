@@ -810,7 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Kv8AttnA
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&ms.part_full[k], 1);
-      mbar_init(&ms.part_free[k], C::kMT * 4 + kConvert / 32 + 1);  // the warps of the softmax, of the conversion, the products'
+      // the warps of the softmax, of the conversion, the products'
+      mbar_init(&ms.part_free[k], C::kMT * 4 + kConvert / 32 + 1);
       mbar_init(&ms.o_free[0][k], 128);
       mbar_init(&ms.o_free[1][k], 128);
       mbar_init(&ms.q_full[k], C::kMT * 128);

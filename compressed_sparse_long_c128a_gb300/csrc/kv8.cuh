@@ -131,7 +131,8 @@ __device__ __forceinline__ float tanh_exp2(float x) { return fmaf(-2.0f, fast_rc
 // the multipliers alone, which stand idle where exponentials are the limit.
 constexpr float kTanhSmall = 0.75f;
 __device__ __forceinline__ float2 tanh_small2(float2 x) {
-  constexpr float c[6] = {0.9999998211860657f, -0.33332470059394836f, 0.13320578634738922f, -0.05314924940466881f, 0.01923721469938755f, -0.00449344189837575f};
+  constexpr float c[6] = {0.9999998211860657f,   -0.33332470059394836f, 0.13320578634738922f,
+                          -0.05314924940466881f, 0.01923721469938755f,  -0.00449344189837575f};
   const float2 s = mul2(x, x);
   float2 p = make_float2(c[5], c[5]);
 #pragma unroll
